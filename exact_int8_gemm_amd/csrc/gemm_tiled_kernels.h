@@ -109,13 +109,6 @@ __device__ inline void tile_of_split(int tiles_m, int tiles_n, int splits, int& 
 __device__ inline float half_bits_to_float(uint16_t h) { return (float)__builtin_bit_cast(_Float16, h); }
 
 
-// Buffer resource over `bytes` bytes from `base` (raw, stride 0); accesses at
-// offsets past the end return zero.  Clamped below kOutOfRange.
-__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
-  const int64_t n = bytes < (int64_t)kOutOfRange - 1 ? bytes : (int64_t)kOutOfRange - 1;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
-}
-
 // One BK slice of the A (activation) and B (weight) tiles, held in registers
 // between its global loads and its LDS stores.  Loads are branch-free buffer
 // loads: a row outside the matrix has an out-of-range base offset and a

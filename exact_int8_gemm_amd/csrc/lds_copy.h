@@ -10,6 +10,13 @@ namespace tiled {
 // Byte offset that a buffer access treats as out of range: loads return 0.
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
+// Buffer resource over `bytes` bytes from `base` (raw, stride 0); accesses at
+// offsets past the end return zero.  Clamped below kOutOfRange.
+__device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  const int64_t n = bytes < (int64_t)kOutOfRange - 1 ? bytes : (int64_t)kOutOfRange - 1;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
+}
+
 namespace dma {
 
 // Raw buffer resource as four dwords (raw, stride 0): base address, bounds

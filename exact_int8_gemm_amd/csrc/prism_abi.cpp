@@ -69,6 +69,28 @@ int check_gemm(const void* q, const void* s_a, const void* w, const void* scale_
   return PRISM_OK;
 }
 
+bool known_type(int t) { return t == PRISM_TYPE_F32 || t == PRISM_TYPE_F16 || t == PRISM_TYPE_BF16; }
+int64_t type_size(int t) { return t == PRISM_TYPE_F32 ? 4 : 2; }
+
+// Checks of the fp8 quantizers (x2: the second input of SwiGLU, else x again).
+// group_rows bounds the grid: one workgroup per group_rows rows and 128 k.
+int check_fp8_quant(const void* x, const void* x2, int type, int64_t ld, const void* q, const void* scale, int64_t M,
+                    int64_t K, int group_rows, bool* noop) {
+  *noop = false;
+  if (!known_type(type) || M < 0 || K < 0) return PRISM_ERR_INVALID_ARG;
+  if (M == 0) {
+    *noop = true;
+    return PRISM_OK;
+  }
+  if (K == 0 || K > PRISM_K_MAX || M > INT_MAX || ld < K || ld > INT64_MAX / 4 / M) return PRISM_ERR_INVALID_ARG;
+  if (!x || !x2 || !q || !scale) return PRISM_ERR_INVALID_ARG;
+  if ((M + group_rows - 1) / group_rows * ((K + 127) / 128) > INT_MAX) return PRISM_ERR_INVALID_ARG;  // grid size
+  if (K % 16 != 0 || !aligned(x, 16) || !aligned(x2, 16) || ld * type_size(type) % 16 != 0 || !aligned(q, 16) ||
+      !aligned(scale, 4))
+    return PRISM_ERR_ALIGNMENT;
+  return PRISM_OK;
+}
+
 // Grid limits of the tiled kernels (64 x 128 tiles with a 4-way K split at the most).
 bool grid_fits(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 127) / 128) * 4 <= INT_MAX; }
 
@@ -146,7 +168,9 @@ const char* prism_build_id(void) { return PRISM_BUILD_ID; }
 const char* prism_status_string(int status) {
   switch (status) {
     case PRISM_OK: return "ok";
-    case PRISM_ERR_INVALID_ARG: return "invalid argument (null pointer, negative or zero size, or K above PRISM_K_MAX)";
+    case PRISM_ERR_INVALID_ARG:
+      return "invalid argument (null pointer, negative or zero size, K above PRISM_K_MAX, unknown type, row stride "
+             "below the row, or workspace too small)";
     case PRISM_ERR_ALIGNMENT: return "misaligned pointer or K not a multiple of the required block";
     case PRISM_ERR_UNSUPPORTED: return "no usable gfx950 (MI355X) device is current";
     case PRISM_ERR_LAUNCH: return "kernel launch failed";
@@ -295,6 +319,75 @@ int prism_gemm_w8a8_blockscale(const int8_t* q, const float* s_a, const int8_t* 
   if ((st = check_device()) != PRISM_OK) return st;
   return prism::launch_gemm_blockscale(q, s_a, w, d, y, partials, (int)M, (int)N, (int)K,
                                        static_cast<hipStream_t>(stream));
+}
+
+int prism_quantize_blocks_fp8(const void* x, int x_type, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,
+                              void* stream) {
+  bool noop;
+  int st = check_fp8_quant(x, x, x_type, ld, q, scale, M, K, 16, &noop);
+  if (st != PRISM_OK || noop) return st;
+  if ((st = check_device()) != PRISM_OK) return st;
+  return prism::launch_quantize_blocks_fp8(x, x_type, ld, q, scale, M, K, static_cast<hipStream_t>(stream));
+}
+
+int prism_quantize_tiles_fp8(const void* x, int x_type, int64_t ld, uint8_t* q, float* scale, int64_t N, int64_t K,
+                             void* stream) {
+  bool noop;
+  int st = check_fp8_quant(x, x, x_type, ld, q, scale, N, K, 128, &noop);
+  if (st != PRISM_OK || noop) return st;
+  if ((st = check_device()) != PRISM_OK) return st;
+  return prism::launch_quantize_tiles_fp8(x, x_type, ld, q, scale, N, K, static_cast<hipStream_t>(stream));
+}
+
+int prism_swiglu_quantize_fp8(const void* gate, const void* up, int x_type, int64_t ld, uint8_t* q, float* scale,
+                              int64_t M, int64_t K, void* stream) {
+  bool noop;
+  int st = check_fp8_quant(gate, up, x_type, ld, q, scale, M, K, 16, &noop);
+  if (st != PRISM_OK || noop) return st;
+  if ((st = check_device()) != PRISM_OK) return st;
+  return prism::launch_swiglu_quantize_fp8(gate, up, x_type, ld, q, scale, M, K, static_cast<hipStream_t>(stream));
+}
+
+int prism_gemm_fp8_blockscale(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y,
+                              int y_type, int64_t M, int64_t N, int64_t K, void* stream) {
+  if (!known_type(y_type)) return PRISM_ERR_INVALID_ARG;
+  bool noop;
+  // y's alignment is checked below: 2 bytes are enough for a 16-bit y
+  int st = check_gemm(q, s_a, w, s_w, y ? q : nullptr, nullptr, M, N, K, 16, &noop);
+  if (st != PRISM_OK || noop) return st;
+  if (!aligned(s_w, 4) || !aligned(y, type_size(y_type))) return PRISM_ERR_ALIGNMENT;
+  if (((M + 15) / 16) * ((N + 15) / 16) > INT_MAX) return PRISM_ERR_INVALID_ARG;  // grid size
+  if ((st = check_device()) != PRISM_OK) return st;
+  return prism::launch_gemm_fp8(q, s_a, w, s_w, y, y_type, (int)M, (int)N, (int)K, static_cast<hipStream_t>(stream));
+}
+
+int prism_token_logprobs_workspace(int64_t M, int64_t V, int top, int64_t* bytes) {
+  if (M < 0 || V < 0 || M > INT_MAX || V > INT_MAX || top < 0 || top > PRISM_TOP_MAX || !bytes)
+    return PRISM_ERR_INVALID_ARG;
+  *bytes = prism::token_logprobs_bytes(M, V, top);
+  return PRISM_OK;
+}
+
+int prism_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t T, int top,
+                         float* logprobs, float* lse, float* entropy, int64_t* top_ids, float* top_logprobs,
+                         void* workspace, int64_t workspace_bytes, int64_t M, int64_t V, void* stream) {
+  if (!known_type(type) || M < 0 || V < 0 || T < 0 || top < 0 || top > PRISM_TOP_MAX || workspace_bytes < 0)
+    return PRISM_ERR_INVALID_ARG;
+  if (M == 0) return PRISM_OK;
+  if (V == 0 || M > INT_MAX || V > INT_MAX || T > INT_MAX || ld < V || ld > INT64_MAX / 4 / M)
+    return PRISM_ERR_INVALID_ARG;
+  if (!logits || (T > 0 && (!tokens || !logprobs)) || (top > 0 && (!top_ids || !top_logprobs)))
+    return PRISM_ERR_INVALID_ARG;
+  const int64_t need = prism::token_logprobs_bytes(M, V, top);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return PRISM_ERR_INVALID_ARG;
+  if (!prism::token_logprobs_grid_fits(M, V)) return PRISM_ERR_INVALID_ARG;
+  if (!aligned(logits, type_size(type)) || !aligned(tokens, 8) || !aligned(logprobs, 4) || !aligned(lse, 4) ||
+      !aligned(entropy, 4) || !aligned(top_ids, 8) || !aligned(top_logprobs, 4) || !aligned(workspace, 8))
+    return PRISM_ERR_ALIGNMENT;
+  const int dev = check_device();
+  if (dev != PRISM_OK) return dev;
+  return prism::launch_token_logprobs(logits, type, ld, tokens, T, top, logprobs, lse, entropy, top_ids, top_logprobs,
+                                      workspace, M, V, static_cast<hipStream_t>(stream));
 }
 
 int prism_peak_mfma(int64_t iters, int waves_per_simd, int seed, uint32_t* out, void* stream) {

@@ -83,6 +83,21 @@ int launch_gemm_tiled_variant(const int8_t* q, const float* s_a, const void* w, 
 int launch_gemm_blockscale(const int8_t* q, const float* s_a, const int8_t* w, const uint16_t* d, float* y,
                            int32_t* partials, int M, int N, int K, hipStream_t st);
 
+// fp8 (e4m3) block-128 layer and the token read-out.  `type` is a PRISM_TYPE_*.
+int launch_quantize_blocks_fp8(const void* x, int type, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,
+                               hipStream_t st);
+int launch_quantize_tiles_fp8(const void* x, int type, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,
+                              hipStream_t st);
+int launch_swiglu_quantize_fp8(const void* gate, const void* up, int type, int64_t ld, uint8_t* q, float* scale,
+                               int64_t M, int64_t K, hipStream_t st);
+int launch_gemm_fp8(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int type, int M,
+                    int N, int K, hipStream_t st);
+int64_t token_logprobs_bytes(int64_t M, int64_t V, int top);
+bool token_logprobs_grid_fits(int64_t M, int64_t V);
+int launch_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t ntok, int top,
+                          float* lp, float* lse, float* ent, int64_t* top_ids, float* top_lp, void* ws, int64_t M,
+                          int64_t V, hipStream_t st);
+
 // Measurement kernels (peaks.hip).
 int launch_peak_mfma(int64_t iters, int waves_per_simd, int seed, uint32_t* out, hipStream_t st);
 int launch_peak_read(const void* buf, int64_t bytes, uint32_t* parts, int nparts, hipStream_t st);

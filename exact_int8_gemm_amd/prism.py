@@ -9,6 +9,7 @@ raises instead of computing elsewhere.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 
@@ -18,7 +19,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libprism.so")
 
 PRISM_OK = 0
-ABI_VERSION = 13
+ABI_VERSION = 14
 K_MAX = 131040
 
 # Dispatch-table entries of the W8A8 / W4A8 calls (PRISM_VARIANT_* in include/prism.h).
@@ -68,6 +69,18 @@ def _declare(lib):
         fn = getattr(lib, name)
         fn.restype = i32
         fn.argtypes = [p, p, p, p, p, p, i64, i64, i64, p]
+    for name in ("prism_quantize_blocks_fp8", "prism_quantize_tiles_fp8"):
+        fn = getattr(lib, name)
+        fn.restype = i32
+        fn.argtypes = [p, i32, i64, p, p, i64, i64, p]
+    lib.prism_swiglu_quantize_fp8.restype = i32
+    lib.prism_swiglu_quantize_fp8.argtypes = [p, p, i32, i64, p, p, i64, i64, p]
+    lib.prism_gemm_fp8_blockscale.restype = i32
+    lib.prism_gemm_fp8_blockscale.argtypes = [p, p, p, p, p, i32, i64, i64, i64, p]
+    lib.prism_token_logprobs_workspace.restype = i32
+    lib.prism_token_logprobs_workspace.argtypes = [i64, i64, i32, ctypes.POINTER(i64)]
+    lib.prism_token_logprobs.restype = i32
+    lib.prism_token_logprobs.argtypes = [p, i32, i64, p, i64, i32, p, p, p, p, p, p, i64, i64, i64, p]
     lib.prism_peak_mfma.restype = i32
     lib.prism_peak_mfma.argtypes = [i64, i32, i32, p, p]
     lib.prism_peak_read.restype = i32
@@ -317,6 +330,148 @@ def gemm_w8a8_blockscale(q, s_a, w, d, y=None, partials=None):
         _check(lib().prism_gemm_w8a8_blockscale(_ptr(q), _ptr(s_a), _ptr(w), _ptr(d), _ptr(y), _ptr(partials),
                                                 M, N, K, _stream(dev)))
     return y
+
+
+# ------------------------------------------------------- 8-bit floating point layer
+
+FP8 = torch.float8_e4m3fn
+FP8_BLOCK = 128
+TOP_MAX = 32
+TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _blocks(n):
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def _rows(x, name):
+    """A 2-D float tensor on the GPU with contiguous rows (any row stride >= the row) -> (device, rows, cols, stride)."""
+    dev = _gpu(x, name)
+    if x.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    if x.dtype not in TYPES:
+        raise TypeError("%s must be float32, float16 or bfloat16, got %s" % (name, x.dtype))
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    # the stride of a single row is never used and may be anything
+    ld = x.stride(0) if rows > 1 else cols
+    if rows > 1 and ld < cols:
+        raise ValueError("%s has overlapping rows (row stride %d, %d columns)" % (name, ld, cols))
+    return dev, rows, cols, ld
+
+
+def _fp8_outputs(q, scale, M, K, scale_shape, dev):
+    q = torch.empty((M, K), dtype=FP8, device=dev) if q is None else _need(q, "q", FP8, (M, K), dev)
+    scale = (torch.empty(scale_shape, dtype=torch.float32, device=dev) if scale is None
+             else _need(scale, "scale", torch.float32, scale_shape, dev))
+    return q, scale
+
+
+def quantize_blocks_fp8(x, q=None, scale=None):
+    """x float32/float16/bfloat16 [M, K] on the GPU (rows may be strided) -> (q float8_e4m3fn [M, K],
+    scale float32 [ceil(K/128), M]): one scale per 128 consecutive values of a row."""
+    dev, M, K, ld = _rows(x, "x")
+    q, scale = _fp8_outputs(q, scale, M, K, (_blocks(K), M), dev)
+    with torch.cuda.device(dev):
+        _check(lib().prism_quantize_blocks_fp8(_ptr(x), TYPES[x.dtype], ld, _ptr(q), _ptr(scale), M, K, _stream(dev)))
+    return q, scale
+
+
+def quantize_tiles_fp8(w, q=None, scale=None):
+    """w float32/float16/bfloat16 [N, K] on the GPU (rows may be strided) -> (q float8_e4m3fn [N, K],
+    scale float32 [ceil(N/128), ceil(K/128)]): one scale per 128 x 128 tile."""
+    dev, N, K, ld = _rows(w, "w")
+    q, scale = _fp8_outputs(q, scale, N, K, (_blocks(N), _blocks(K)), dev)
+    with torch.cuda.device(dev):
+        _check(lib().prism_quantize_tiles_fp8(_ptr(w), TYPES[w.dtype], ld, _ptr(q), _ptr(scale), N, K, _stream(dev)))
+    return q, scale
+
+
+def swiglu_quantize_fp8(gate, up, q=None, scale=None):
+    """gate, up [M, K] of one float type and one row stride (the halves of one [M, 2K] product) ->
+    quantize_blocks_fp8 of silu(gate) * up, in one pass."""
+    dev, M, K, ld = _rows(gate, "gate")
+    dev2, M2, K2, ld2 = _rows(up, "up")
+    if up.dtype != gate.dtype:
+        raise TypeError("up must be %s like gate, got %s" % (gate.dtype, up.dtype))
+    if dev2 != dev:
+        raise ValueError("up must be on %s, got %s" % (dev, dev2))
+    if (M2, K2) != (M, K):
+        raise ValueError("up must have shape %s, got %s" % ((M, K), (M2, K2)))
+    if ld2 != ld:
+        raise ValueError("gate and up must have the same row stride, got %d and %d" % (ld, ld2))
+    q, scale = _fp8_outputs(q, scale, M, K, (_blocks(K), M), dev)
+    with torch.cuda.device(dev):
+        _check(lib().prism_swiglu_quantize_fp8(_ptr(gate), _ptr(up), TYPES[gate.dtype], ld, _ptr(q), _ptr(scale), M, K,
+                                               _stream(dev)))
+    return q, scale
+
+
+def gemm_fp8_blockscale(q, s_a, w, s_w, y=None, out_dtype=torch.float32):
+    """q float8_e4m3fn [M,K], s_a f32 [ceil(K/128), M], w float8_e4m3fn [N,K], s_w f32 [ceil(N/128), ceil(K/128)]
+    -> y [M,N] of out_dtype (or of y's type, if y is given): float32, float16 or bfloat16."""
+    dev = _gpu(q, "q")
+    if q.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("q and w must be 2-D")
+    M, K = q.shape
+    N = w.shape[0]
+    _need(q, "q", FP8, (M, K), dev)
+    _need(s_a, "s_a", torch.float32, (_blocks(K), M), dev)
+    _need(w, "w", FP8, (N, K), dev)
+    _need(s_w, "s_w", torch.float32, (_blocks(N), _blocks(K)), dev)
+    dtype = out_dtype if y is None else getattr(y, "dtype", None)
+    if dtype not in TYPES:
+        raise TypeError("y must be float32, float16 or bfloat16, got %s" % (dtype,))
+    y = torch.empty((M, N), dtype=dtype, device=dev) if y is None else _need(y, "y", dtype, (M, N), dev)
+    with torch.cuda.device(dev):
+        _check(lib().prism_gemm_fp8_blockscale(_ptr(q), _ptr(s_a), _ptr(w), _ptr(s_w), _ptr(y), TYPES[dtype], M, N, K,
+                                               _stream(dev)))
+    return y
+
+
+# -------------------------------------------------------------------- token read-out
+
+TokenLogprobs = collections.namedtuple("TokenLogprobs", "logprobs lse entropy top_ids top_logprobs")
+
+
+def token_logprobs(logits, tokens=None, top=0, workspace=None):
+    """logits float32/float16/bfloat16 [M, V] on the GPU (rows may be strided) ->
+    TokenLogprobs(logprobs f32 [M, T], lse f32 [M], entropy f32 [M], top_ids int64 [M, top],
+    top_logprobs f32 [M, top]) for the given tokens int64 [M, T] (None: T = 0) and the `top` largest
+    logits.  workspace: a uint8 tensor of at least token_logprobs_workspace(M, V, top) bytes to use
+    instead of a new one."""
+    dev, M, V, ld = _rows(logits, "logits")
+    T = 0
+    if tokens is not None:
+        if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
+            raise ValueError("tokens must be a 2-D tensor")
+        T = tokens.shape[1]
+        _need(tokens, "tokens", torch.int64, (M, T), dev)
+    top = int(top)
+    need = token_logprobs_workspace(M, V, top)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    else:
+        _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    r = TokenLogprobs(torch.empty((M, T), dtype=torch.float32, device=dev),
+                      torch.empty((M,), dtype=torch.float32, device=dev),
+                      torch.empty((M,), dtype=torch.float32, device=dev),
+                      torch.empty((M, top), dtype=torch.int64, device=dev),
+                      torch.empty((M, top), dtype=torch.float32, device=dev))
+    with torch.cuda.device(dev):
+        _check(lib().prism_token_logprobs(_ptr(logits), TYPES[logits.dtype], ld, _ptr(tokens), T, top,
+                                          _ptr(r.logprobs), _ptr(r.lse), _ptr(r.entropy), _ptr(r.top_ids),
+                                          _ptr(r.top_logprobs), _ptr(workspace),
+                                          0 if workspace is None else workspace.numel(), M, V, _stream(dev)))
+    return r
+
+
+def token_logprobs_workspace(M, V, top):
+    """Bytes of scratch memory that token_logprobs needs for these sizes (0: none)."""
+    n = ctypes.c_int64(0)
+    _check(lib().prism_token_logprobs_workspace(M, V, top, ctypes.byref(n)))
+    return n.value
 
 
 # ------------------------------------------------------------ measurement kernels

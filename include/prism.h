@@ -14,8 +14,10 @@
  * Conventions shared by every call:
  *   - Every pointer argument is a DEVICE pointer (HBM of the current HIP
  *     device).  The caller allocates and owns all buffers; the library keeps
- *     no pointer after the call returns and allocates nothing.
- *   - Matrices are dense and row-major with no padding: x, q are [M][K],
+ *     no pointer after the call returns and allocates nothing (the one call
+ *     that needs scratch memory takes it as an argument).
+ *   - Except where a row stride is an argument, matrices are dense and
+ *     row-major with no padding: x, q are [M][K],
  *     w is [N][K], w4 is [N][K/2], d is [N][K/32], y and acc are [M][N],
  *     partials is [M][N][K/32].
  *   - x, q, w and w4 must be 16-byte aligned; every other pointer must be
@@ -42,15 +44,23 @@ extern "C" {
 #endif
 
 /* Bumped on any change of a signature or of the semantics below. */
-#define PRISM_ABI_VERSION 13
+#define PRISM_ABI_VERSION 14
 
 /* Largest accepted K.  For K <= 131040 every exact sum of K products of two
  * int8 values (|q|, |w| <= 128) lies strictly inside the int32 range. */
 #define PRISM_K_MAX 131040
 
+/* Element types of the fp8 and read-out calls' wider operands. */
+#define PRISM_TYPE_F32 0
+#define PRISM_TYPE_F16 1  /* IEEE binary16 */
+#define PRISM_TYPE_BF16 2 /* bfloat16 */
+
+/* Largest number of top alternatives of prism_token_logprobs. */
+#define PRISM_TOP_MAX 32
+
 /* Status codes. */
 #define PRISM_OK 0
-#define PRISM_ERR_INVALID_ARG (-1) /* null required pointer, negative size, N or K = 0 with M > 0, K > PRISM_K_MAX */
+#define PRISM_ERR_INVALID_ARG (-1) /* null required pointer, negative size, N or K = 0 with M > 0, K > PRISM_K_MAX, unknown type, row stride below the row, workspace too small */
 #define PRISM_ERR_ALIGNMENT (-2)   /* misaligned pointer, or K not a multiple of 16 (32 for block-scale and W4A8, 256 for Q4_K) */
 #define PRISM_ERR_UNSUPPORTED (-3) /* the current device is not gfx950, or no device is usable */
 #define PRISM_ERR_LAUNCH (-4)      /* the kernel launch reported an error */
@@ -271,6 +281,95 @@ int prism_gemm_w8a8_variant(const int8_t* q, const float* s_a, const int8_t* w, 
 int prism_gemm_w4a8_variant(const int8_t* q, const float* s_a, const uint8_t* w4, const float* s_w,
                             float* y, int32_t* acc, int64_t M, int64_t N, int64_t K, int variant,
                             void* stream);
+
+/*
+ * ---- 8-bit floating point: e4m3 codes with one scale per 128 values ----
+ *
+ * The 8-bit floating point form of the same layer (StartLux-Prism README, "Why
+ * StartLux-Prism": quantized weights and activations, a row's result
+ * independent of its batch; the pages keep 8-bit floats to the KV cache and
+ * give no layout, so the one below is this library's reading).  Codes are OCP
+ * e4m3 bytes (largest value 448, no infinities, NaN 0x7f / 0xff).  KB =
+ * ceil(K / 128) and NB = ceil(N / 128) count blocks; the last ones may be
+ * partial.  x_type is the PRISM_TYPE_* of x.  x may have padded rows: row m
+ * starts ld >= K elements after row m - 1, with the rows 16-byte aligned (x
+ * 16-byte aligned, ld * element size a multiple of 16).  K must be a multiple
+ * of 16 and at most PRISM_K_MAX; q and w are dense and 16-byte aligned.
+ *
+ * Codes of a group of values with largest magnitude a: s = a / 448 (IEEE
+ * fp32 division); code = the e4m3 value nearest (ties to even) to x / s, the
+ * correctly rounded fp32 quotient clamped to +-448.  s = 0 gives codes 0.  A
+ * group holding a NaN or an infinity gets s = NaN and codes 0.  A zero code
+ * may be 0x00 or 0x80.  Groups never influence each other.
+ *
+ * prism_quantize_blocks_fp8: activations, one group per 128 consecutive k of
+ * a row.
+ *   x      [M][K] of x_type, rows ld elements apart.
+ *   q      [M][K] e4m3, output.
+ *   scale  [KB][M] fp32, output: block-major, so that the rows of a tile find
+ *          a block's scales in one piece.
+ */
+int prism_quantize_blocks_fp8(const void* x, int x_type, int64_t ld, uint8_t* q, float* scale,
+                              int64_t M, int64_t K, void* stream);
+
+/*
+ * Weights (see above), one group per 128 x 128 tile.
+ *   x      [N][K] of x_type, rows ld elements apart.
+ *   q      [N][K] e4m3, output;  scale [NB][KB] fp32, output.
+ * N = 0 is a no-op.
+ */
+int prism_quantize_tiles_fp8(const void* x, int x_type, int64_t ld, uint8_t* q, float* scale,
+                             int64_t N, int64_t K, void* stream);
+
+/*
+ * SwiGLU and the activation quantizer behind it, in one pass: what stands
+ * between the two products of a gated MLP.
+ *   gate, up [M][K] of x_type, rows of both ld elements apart (the halves of
+ *            one [M][2 K] product: up = gate + K, ld = 2 K).
+ *   q, scale as prism_quantize_blocks_fp8 of h = gate / (1 + exp(-gate)) * up,
+ *            computed in fp32.
+ */
+int prism_swiglu_quantize_fp8(const void* gate, const void* up, int x_type, int64_t ld, uint8_t* q, float* scale,
+                              int64_t M, int64_t K, void* stream);
+
+/*
+ * GEMM on those codes and scales.
+ *   q [M][K] e4m3, s_a [KB][M] fp32; w [N][K] e4m3, s_w [NB][KB] fp32.
+ *   y [M][N] of y_type (PRISM_TYPE_*), output, aligned to its element size.
+ * P_b = the sum of block b's products; f = +0; for b ascending f =
+ * fmaf(P_b, s_a[b][m] * s_w[n / 128][b], f); y[m][n] = f, rounded once to
+ * y_type.  With y_type fp32 the products are exact and P_b is an fp32 sum.
+ * With a 16-bit y_type P_b is the matrix cores' fp8 sum, which aligns its
+ * products to the largest: its error is up to about 2^-10 of the block's
+ * largest product, below the rounding of y except where sums cancel.  Rows
+ * have the same bits whatever M is (fp32 and 16-bit y are two functions).
+ */
+int prism_gemm_fp8_blockscale(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w,
+                              void* y, int y_type, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * Token read-out: log probabilities of given tokens, entropy and top
+ * alternatives of each row of logits (README "Example": answers are read
+ * from the probabilities of given tokens).
+ *   logits [M][V] of `type`, rows ld >= V elements apart, aligned to their
+ *          element size only (V may be odd).  A masked entry is -inf.
+ *   tokens [M][T] int64, or NULL with T = 0.
+ *   logprobs [M][T] fp32: z_t - log sum exp z; NaN for a token outside [0, V).
+ *   lse, entropy [M] fp32, each may be NULL: log sum exp z, -sum p log p.
+ *   top_ids [M][top] int64, top_logprobs [M][top] fp32 (0 <= top <=
+ *          PRISM_TOP_MAX; NULL with top = 0): the largest logits, largest
+ *          first, the lower index first among equals.  Slots past the last
+ *          entry of nonzero probability hold -1 and -inf.
+ *   workspace  prism_token_logprobs_workspace bytes (8-byte aligned; may be
+ *          NULL if that is 0), free again when the stream passes the call.
+ * All sums are fp32 in an order that depends on V and `type` only.  A row with every entry -inf:
+ * logprobs and lse -inf, entropy 0.  A row with a NaN or +inf: all NaN, and
+ * ids -1.
+ */
+int prism_token_logprobs_workspace(int64_t M, int64_t V, int top, int64_t* bytes);
+int prism_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t T, int top,
+                         float* logprobs, float* lse, float* entropy, int64_t* top_ids, float* top_logprobs,
+                         void* workspace, int64_t workspace_bytes, int64_t M, int64_t V, void* stream);
 
 /*
  * Measurement kernels (not part of the GEMM path): what this GPU reaches on

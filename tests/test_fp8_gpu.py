@@ -1,0 +1,510 @@
+"""The fp8 (e4m3) quantizers, SwiGLU and GEMM on the GPU against plain 64-bit references.
+
+Tolerances.  Codes and scales of the quantizers are compared exactly (the
+definition is a chain of single fp32 roundings); SwiGLU's codes may be one
+e4m3 step off where h's own error (exp and division in fp32, taken as 2^-18
+relative) moves x / s over a tie.
+
+GEMM, fp32 y: products are exact; the sum of 128 of them, whatever its order,
+is off by at most 128 roundings of 2^-23 (directed rounding allowed) of
+sum |a b|; the fold adds one half-step 2^-24 per block and one for the scale
+product.  All relative to T = sum |a b s s|:
+    |y - exact| <= (128 * 2^-23 + (KB + 2) * 2^-24) T.
+16-bit y: the matrix cores align the products of a block to the largest one;
+a product cut at 2^-12 of it loses at most half that, 128 of them 2^-6 in the
+worst case.  With the rounding of y:
+    |y - exact| <= 2^-6 * peaks + (as above) T + eps / 2 * |exact| + the
+smallest subnormal of f16.  That worst case is far from what random operands
+show, so the 2-norm is bounded too: one rounding of y and 1e-4 for the sums.
+"""
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+from exact_int8_gemm_amd import prism
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+EPS = {"f32": 2.0 ** -23, "f16": 2.0 ** -10, "bf16": 2.0 ** -7}
+
+
+def host(t):
+    return (t.float() if t.dtype in (torch.bfloat16, torch.float16, prism.FP8) else t).cpu().numpy()
+
+
+def as_fp8(values):
+    """Exact e4m3 values (numpy) -> float8_e4m3fn on the GPU."""
+    return torch.from_numpy(np.ascontiguousarray(values, np.float32)).to(prism.FP8).to(DEV)
+
+
+def bits(t):
+    return t.contiguous().view(torch.int16 if t.element_size() == 2 else torch.int32)
+
+
+# --------------------------------------------------------------- quantizers
+
+def quant_input(rng, m, k):
+    x = rng.standard_normal((m, k)).astype(np.float32) * np.exp(rng.uniform(-20, 20, (m, 1))).astype(np.float32)
+    x[:, rng.random(k) < 0.02] *= 50
+    return x
+
+
+QUANT_SHAPES = [(1, 16), (1, 128), (2, 112), (3, 144), (16, 256), (17, 400), (33, 1040), (130, 2064), (257, 640),
+                (1, 5120), (5, 17408)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,k", QUANT_SHAPES)
+def test_quantize_blocks(m, k, kind):
+    rng = np.random.default_rng(m * 1000 + k)
+    x = torch.from_numpy(quant_input(rng, m, k)).to(TYPES[kind]).to(DEV)
+    if kind == "f16":
+        x = x.clamp(-60000, 60000)
+    q, s = prism.quantize_blocks_fp8(x)
+    v, sr = ref.quantize(host(x), 1)
+    assert np.array_equal(host(s), sr.T)
+    assert np.array_equal(host(q), v.astype(np.float32))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("n,k", [(1, 16), (100, 128), (128, 144), (129, 256), (300, 400), (257, 2064), (640, 5120)])
+def test_quantize_tiles(n, k, kind):
+    rng = np.random.default_rng(n * 1000 + k)
+    x = torch.from_numpy(rng.standard_normal((n, k)).astype(np.float32) * 0.02).to(TYPES[kind]).to(DEV)
+    q, s = prism.quantize_tiles_fp8(x)
+    v, sr = ref.quantize(host(x), 128)
+    assert np.array_equal(host(s), sr)
+    assert np.array_equal(host(q), v.astype(np.float32))
+
+
+@pytest.mark.parametrize("rows", [1, 128])
+def test_quantize_special_values(rows):
+    """NaN, infinities, zeros, subnormals and the largest values, each in a block or tile of its own."""
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((rows * 4, 128 * 5)).astype(np.float32)
+    b = [slice(128 * i, 128 * i + 128) for i in range(5)]
+    r = [slice(rows * i, rows * i + rows) for i in range(4)]
+    x[rows * 0, 3] = np.nan
+    x[rows * 0, 128 + 127] = np.inf
+    x[rows * 0, 256] = -np.inf
+    x[r[0], b[3]] = 0
+    x[r[0], b[4]] = -0.0
+    x[r[1], b[0]] *= np.float32(1e-40)          # subnormal values, subnormal scale
+    x[r[1], b[1]] = 0
+    x[rows, 128 + 5] = np.float32(1.4e-45)      # amax / 448 underflows to 0
+    x[r[1], b[2]] = 0
+    x[rows, 256 + 9] = np.float32(900 * 1.4e-45)    # scale 2 * 2^-149
+    x[r[1], b[3]] *= np.float32(1e-27)          # around 2^-90
+    x[r[1], b[4]] *= np.float32(1e-25)
+    x[rows * 2, 7] = np.finfo(np.float32).max
+    x[rows * 2, 130] = -np.finfo(np.float32).max
+    x[r[2], b[2]] = np.float32(3.0)             # every value the largest
+    fn = prism.quantize_blocks_fp8 if rows == 1 else prism.quantize_tiles_fp8
+    q, s = fn(torch.from_numpy(x).to(DEV))
+    v, sr = ref.quantize(x, rows)
+    got_s = host(s).T if rows == 1 else host(s)
+    assert np.array_equal(got_s, sr, equal_nan=True)
+    assert np.isnan(sr[0, :3]).all() and np.isfinite(sr[0, 3:]).all()
+    assert np.array_equal(host(q), v.astype(np.float32))
+
+
+def test_quantize_ties():
+    """x placed at every rounding tie of x / s and one fp32 step to each side, for scales with full mantissas."""
+    rng = np.random.default_rng(6)
+    rowsets = []
+    for amax in (448.0, 447.3, 1.0, 0.7310586, 3.1e-5, 9.87e20):
+        s = np.float32(amax) / np.float32(448)
+        t = (ref._MID[rng.permutation(126)[:126]] * np.float64(s)).astype(np.float32)
+        for step in (0, 1, -1):
+            y = t.copy()
+            if step:
+                y = np.nextafter(y, np.float32(step * np.inf))
+            row = np.zeros(128, np.float32)
+            row[:126] = np.where(rng.random(126) < 0.5, y, -y)
+            row[126] = np.float32(amax)
+            rowsets.append(row)
+    x = np.stack(rowsets)
+    q, s = prism.quantize_blocks_fp8(torch.from_numpy(x).to(DEV))
+    v, sr = ref.quantize(x, 1)
+    assert np.array_equal(host(s), sr.T)
+    assert np.array_equal(host(q), v.astype(np.float32))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_quantize_strided_rows_and_given_outputs(kind):
+    rng = np.random.default_rng(8)
+    big = torch.from_numpy(rng.standard_normal((37, 1024)).astype(np.float32)).to(TYPES[kind]).to(DEV)
+    x = big[:, 256:256 + 400]
+    q = torch.empty((37, 400), dtype=prism.FP8, device=DEV)
+    s = torch.empty((4, 37), dtype=torch.float32, device=DEV)
+    q2, s2 = prism.quantize_blocks_fp8(x, q=q, scale=s)
+    assert q2 is q and s2 is s
+    v, sr = ref.quantize(host(x.contiguous()), 1)
+    assert np.array_equal(host(s), sr.T) and np.array_equal(host(q), v.astype(np.float32))
+    qt, st = prism.quantize_tiles_fp8(x)
+    v, sr = ref.quantize(host(x.contiguous()), 128)
+    assert np.array_equal(host(st), sr) and np.array_equal(host(qt), v.astype(np.float32))
+
+
+def test_quantize_does_not_write_outside():
+    x = torch.randn((19, 272), device=DEV)
+    q = torch.full((19 + 8, 272), 3.0, device=DEV).to(prism.FP8)
+    s = torch.full((3 * 19 + 64,), 7.0, device=DEV)
+    prism.quantize_blocks_fp8(x, q=q[:19], scale=s[:57].view(3, 19))
+    assert (q[19:].float() == 3).all() and (s[57:] == 7).all()
+    prism.quantize_tiles_fp8(x, q=q[:19], scale=s[:3].view(1, 3))
+    assert (q[19:].float() == 3).all() and (s[57:] == 7).all()
+
+
+def swiglu_bounds(h, s, k):
+    """Lowest and highest code value that h (1 +- 2^-18) may give."""
+    sp = ref.spread(s, k)
+    with np.errstate(all="ignore"):
+        t = np.where(sp > 0, h / sp, 0)
+    return ref.round_e4m3(t * (1 - np.sign(t) * 2.0 ** -18)), ref.round_e4m3(t * (1 + np.sign(t) * 2.0 ** -18))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,k", [(1, 16), (1, 9728), (4, 144), (17, 400), (130, 2064)])
+def test_swiglu(m, k, kind):
+    rng = np.random.default_rng(m + k)
+    gu = torch.from_numpy(rng.standard_normal((m, 2 * k)).astype(np.float32) * 4).to(TYPES[kind]).to(DEV)
+    q, s = prism.swiglu_quantize_fp8(gu[:, :k], gu[:, k:])
+    g, u = host(gu[:, :k].contiguous()), host(gu[:, k:].contiguous())
+    h = ref.swiglu(g, u)
+    amax = np.abs(ref._grouped(h, 1)).max(axis=(1, 3)).T
+    assert np.allclose(host(s), amax / 448, rtol=2.0 ** -17, atol=0)
+    lo, hi = swiglu_bounds(h, host(s), k)
+    got = host(q)
+    assert ((got >= lo) & (got <= hi)).all()
+
+
+def test_swiglu_special_values():
+    g = np.zeros((6, 128), np.float32)
+    u = np.ones((6, 128), np.float32)
+    g[0, :4] = [200, -200, 88.8, -103]        # exp(-g) underflows / overflows: h = 200, -0, 88.8, ~0
+    g[1, 0], u[1, 0] = np.nan, 1
+    g[2, 0], u[2, 0] = 1, np.inf
+    g[3, 0], u[3, 0] = np.inf, 1
+    g[4, 0], u[4, 0] = -np.inf, 1             # -inf / (1 + inf) is NaN by the formula
+    g[5, :2], u[5, :2] = [1, 2], [0, 0]
+    q, s = prism.swiglu_quantize_fp8(torch.from_numpy(g).to(DEV), torch.from_numpy(u).to(DEV))
+    q, s = host(q), host(s)[0]
+    assert np.isclose(s[0], 200 / 448, rtol=1e-6) and q[0, 0] == 448 and q[0, 1] == 0 and q[0, 3] == 0
+    assert np.isnan(s[1:5]).all() and not q[1:].any() and s[5] == 0
+
+
+# --------------------------------------------------------------------- GEMM
+
+def gemm_input(rng, m, n, k):
+    x = rng.standard_normal((m, k)).astype(np.float32)
+    x[:, rng.random(k) < 0.01] *= 20
+    q, sa = ref.quantize(x, 1)
+    w, sw = ref.quantize(rng.standard_normal((n, k)).astype(np.float32) * np.float32(0.02), 128)
+    return q, np.ascontiguousarray(sa.T), w, sw
+
+
+def run_gemm(q, sa, w, sw, kind):
+    return prism.gemm_fp8_blockscale(as_fp8(q), torch.from_numpy(sa).to(DEV), as_fp8(w), torch.from_numpy(sw).to(DEV),
+                                     out_dtype=TYPES[kind])
+
+
+def check_gemm(q, sa, w, sw, kind, y):
+    exact, total = ref.gemm(q, sa, w, sw)
+    kb = sa.shape[0]
+    tol = (128 * 2.0 ** -23 + (kb + 2) * 2.0 ** -24) * total
+    err = np.abs(host(y).astype(np.float64) - exact)
+    if kind != "f32":
+        tol = tol + 2.0 ** -6 * ref.block_peaks(q, sa, w, sw) + EPS[kind] / 2 * np.abs(exact) + 2.0 ** -25
+        assert np.linalg.norm(err) <= (EPS[kind] / 2 + 1e-4) * np.linalg.norm(exact) + 2.0 ** -25 * exact.size ** 0.5
+    assert (err <= tol).all(), (float((err / np.maximum(tol, 1e-300)).max()), int((err > tol).sum()))
+
+
+SHAPES = [(1, 1, 16), (1, 16, 128), (1, 129, 5120), (2, 100, 144), (3, 300, 400), (4, 640, 2064), (5, 17, 9680),
+          (7, 1000, 256), (16, 256, 1040), (17, 130, 272), (31, 257, 640), (33, 520, 2576), (64, 128, 4112),
+          (65, 192, 128), (100, 321, 528), (128, 256, 896), (129, 640, 1168), (200, 1300, 384), (257, 300, 2064),
+          (300, 129, 16), (513, 1030, 656), (1000, 700, 1296)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm_against_64_bits(m, n, k, kind):
+    args = gemm_input(np.random.default_rng(m * 7 + n * 3 + k), m, n, k)
+    check_gemm(*args, kind, run_gemm(*args, kind))
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm_exact_on_small_integers(m, n, k, kind):
+    """Codes in {-2 .. 2} and scales that are powers of two: every sum is exact in any order, so y is the rounded
+    exact result bit for bit (every index, scale and edge has to be right)."""
+    rng = np.random.default_rng(m + 10 * n + 100 * k)
+    q = rng.integers(-2, 3, (m, k)).astype(np.float64)
+    w = rng.integers(-2, 3, (n, k)).astype(np.float64)
+    kb, nb = -(-k // 128), -(-n // 128)
+    sa = np.exp2(rng.integers(-2, 3, (kb, m))).astype(np.float32)
+    sw = np.exp2(rng.integers(-2, 3, (nb, kb))).astype(np.float32)
+    y = run_gemm(q, sa, w, sw, kind)
+    exact, _ = ref.gemm(q, sa, w, sw)
+    want = torch.from_numpy(exact).to(TYPES[kind])
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gemm_exact_over_large_shapes(kind):
+    """The same at sizes that take the largest tiles, in torch on the GPU (float64 product)."""
+    for m, n, k in ((2048, 2176, 640), (1500, 5120, 400), (4096, 640, 1168), (8192, 1300, 272), (700, 9728, 528)):
+        g = torch.Generator(device="cuda").manual_seed(m + n + k)
+        q = torch.randint(-2, 3, (m, k), generator=g, device=DEV).double()
+        w = torch.randint(-2, 3, (n, k), generator=g, device=DEV).double()
+        kb, nb = -(-k // 128), -(-n // 128)
+        sa = torch.exp2(torch.randint(-2, 3, (kb, m), generator=g, device=DEV).float())
+        sw = torch.exp2(torch.randint(-2, 3, (nb, kb), generator=g, device=DEV).float())
+        y = prism.gemm_fp8_blockscale(q.float().to(prism.FP8), sa, w.float().to(prism.FP8), sw, out_dtype=TYPES[kind])
+        a = q * sa.t().double().repeat_interleave(128, 1)[:, :k]
+        b = w * sw.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+        assert torch.equal(y, torch.mm(a, b.t().contiguous()).to(TYPES[kind])), (m, n, k)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,k", [(640, 5120), (1300, 2064), (9728, 400), (300, 17408)])
+def test_gemm_rows_do_not_depend_on_the_batch(n, k, kind):
+    """The same 6 rows alone, in fours, and inside batches of many sizes: the same bits, and the same bits twice."""
+    rng = np.random.default_rng(n + k)
+    M = 2300
+    q, sa, w, sw = gemm_input(rng, 64, n, k)
+    pick = rng.integers(0, 64, M)
+    rows = rng.permutation(M)[:6]
+    pick[rows] = np.arange(6)
+    qd, sad = as_fp8(q), torch.from_numpy(sa).to(DEV)
+    wd, swd = as_fp8(w), torch.from_numpy(sw).to(DEV)
+
+    def run(idx):
+        idx = torch.from_numpy(np.asarray(idx)).to(DEV)
+        qi = qd.view(torch.uint8)[idx].view(prism.FP8).contiguous()
+        return bits(prism.gemm_fp8_blockscale(qi, sad[:, idx].contiguous(), wd, swd, out_dtype=TYPES[kind]))
+
+    alone = torch.cat([run([i]) for i in range(6)])
+    assert torch.equal(run(np.arange(4)), alone[:4])
+    for m in (6, 12, 17, 40, 64, 65, 100, 130, 200, 260, 400, 600, 1100):
+        idx = np.concatenate([rng.integers(6, 64, m - 6), np.arange(6)])
+        order = rng.permutation(m)
+        got = run(idx[order])
+        where = np.argsort(order)[m - 6:]
+        assert torch.equal(got[torch.from_numpy(where).to(DEV)], alone), m
+    big = run(pick)
+    assert torch.equal(big[torch.from_numpy(rows).to(DEV)], alone)
+    assert torch.equal(run(pick), big)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gemm_special_values(kind):
+    """A NaN scale (a block with a NaN or infinity) spoils its own row only; a NaN code its row or column; zero
+    scales and the largest codes and scales do what the formula says."""
+    rng = np.random.default_rng(11)
+    for m, n, k in ((5, 300, 400), (40, 300, 400), (300, 300, 400)):
+        q, sa, w, sw = gemm_input(rng, m, n, k)
+        clean = run_gemm(q, sa, w, sw, kind)
+        sa2 = sa.copy()
+        sa2[1, 3] = np.nan
+        y = run_gemm(q, sa2, w, sw, kind)
+        keep = [i for i in range(m) if i != 3]
+        assert torch.isnan(y[3]).all() and torch.equal(y[keep], clean[keep])
+        qd = as_fp8(q).view(torch.uint8).clone()
+        wd = as_fp8(w).view(torch.uint8).clone()
+        qd[2, 399] = 0x7F
+        wd[299, 0] = 0xFF
+        y = prism.gemm_fp8_blockscale(qd.view(prism.FP8), torch.from_numpy(sa).to(DEV), wd.view(prism.FP8),
+                                      torch.from_numpy(sw).to(DEV), out_dtype=TYPES[kind])
+        bad = torch.isnan(y)
+        want = torch.zeros_like(bad)
+        want[2, :] = True
+        want[:, 299] = True
+        assert torch.equal(bad, want) and torch.equal(y[~want], clean[~want])
+        y = run_gemm(q, np.zeros_like(sa), w, sw, kind)
+        assert (y == 0).all()
+        y = run_gemm(np.full((m, k), 448.0), np.full_like(sa, 2.0 ** 60), np.full((n, k), 448.0),
+                     np.full_like(sw, 2.0 ** 60), kind)
+        assert torch.isinf(y).all() or kind == "f32" and (y > 0).all()
+
+
+def test_gemm_does_not_write_outside():
+    rng = np.random.default_rng(12)
+    for m, n, k in ((1, 33, 144), (17, 33, 144), (70, 129, 144), (300, 259, 144)):
+        q, sa, w, sw = gemm_input(rng, m, n, k)
+        for kind in TYPES:
+            buf = torch.full((m * n + 4096,), 5.0, dtype=TYPES[kind], device=DEV)
+            y = buf[:m * n].view(m, n)
+            got = prism.gemm_fp8_blockscale(as_fp8(q), torch.from_numpy(sa).to(DEV), as_fp8(w),
+                                            torch.from_numpy(sw).to(DEV), y=y)
+            assert got is y and (buf[m * n:] == 5).all()
+            check_gemm(q, sa, w, sw, kind, y)
+
+
+def test_gemm_unaligned_16_bit_output():
+    """A 16-bit y that starts at an odd element."""
+    rng = np.random.default_rng(13)
+    for m, n, k in ((3, 33, 144), (70, 129, 272), (300, 256, 272)):
+        q, sa, w, sw = gemm_input(rng, m, n, k)
+        buf = torch.zeros((m * n + 1,), dtype=torch.bfloat16, device=DEV)
+        y = prism.gemm_fp8_blockscale(as_fp8(q), torch.from_numpy(sa).to(DEV), as_fp8(w), torch.from_numpy(sw).to(DEV),
+                                      y=buf[1:].view(m, n))
+        check_gemm(q, sa, w, sw, "bf16", y)
+
+
+def test_gemm_outputs_past_32_bit_offsets():
+    """More than 2^31 outputs: the last rows are the rows of a small call."""
+    m, n, k = 131200, 16500, 16
+    assert m * n > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randint(-2, 3, (m, k), generator=g, device=DEV).float().to(prism.FP8)
+    w = torch.randint(-2, 3, (n, k), generator=g, device=DEV).float().to(prism.FP8)
+    sa = torch.ones((1, m), device=DEV)
+    sw = torch.ones((-(-n // 128), 1), device=DEV)
+    y = prism.gemm_fp8_blockscale(q, sa, w, sw, out_dtype=torch.bfloat16)
+    for r in (0, 65000, m - 300):
+        want = (q[r:r + 300].double() @ w.double().t().contiguous()).to(torch.bfloat16)
+        assert torch.equal(y[r:r + 300], want)
+    del y
+    torch.cuda.empty_cache()
+
+
+def test_quantize_inputs_past_32_bit_offsets():
+    ld, m = 1 << 20, 2100
+    buf = torch.zeros((m * ld,), dtype=torch.bfloat16, device=DEV)
+    x = buf.view(m, ld)[:, 4096:4096 + 144]
+    x.copy_(torch.randn((m, 144), device=DEV))
+    q, s = prism.quantize_blocks_fp8(x)
+    v, sr = ref.quantize(host(x.contiguous()), 1)
+    assert np.array_equal(host(s), sr.T) and np.array_equal(host(q), v.astype(np.float32))
+    qt, st = prism.quantize_tiles_fp8(x)
+    v, sr = ref.quantize(host(x.contiguous()), 128)
+    assert np.array_equal(host(st), sr) and np.array_equal(host(qt), v.astype(np.float32))
+    del x, buf
+    torch.cuda.empty_cache()
+
+
+# ----------------------------------------------------- streams, graphs, refusals
+
+def test_on_a_side_stream():
+    rng = np.random.default_rng(14)
+    x = torch.from_numpy(rng.standard_normal((130, 1040)).astype(np.float32)).to(DEV)
+    w = torch.from_numpy(rng.standard_normal((300, 1040)).astype(np.float32)).to(DEV)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(device=DEV)
+    with torch.cuda.stream(side):
+        x2 = x * 2        # produced on the side stream: the calls have to run behind it
+        q, s = prism.quantize_blocks_fp8(x2)
+        wq, ws = prism.quantize_tiles_fp8(w)
+        y = prism.gemm_fp8_blockscale(q, s, wq, ws)
+    side.synchronize()
+    v, sr = ref.quantize(host(x) * 2, 1)
+    assert np.array_equal(host(q), v.astype(np.float32))
+    check_gemm(host(q), host(s), host(wq), host(ws), "f32", y)
+
+
+def test_graph_replays_match_eager():
+    rng = np.random.default_rng(15)
+    xs = [torch.from_numpy(rng.standard_normal((m, 1040)).astype(np.float32)).to(DEV) for m in (1, 20, 300)]
+    w1 = prism.quantize_tiles_fp8(torch.from_numpy(rng.standard_normal((800, 1040)).astype(np.float32)).to(DEV))
+    w2 = prism.quantize_tiles_fp8(torch.from_numpy(rng.standard_normal((272, 400)).astype(np.float32)).to(DEV))
+
+    def step(x):
+        q, s = prism.quantize_blocks_fp8(x)
+        gu = prism.gemm_fp8_blockscale(q, s, *w1, out_dtype=torch.bfloat16)
+        q2, s2 = prism.swiglu_quantize_fp8(gu[:, :400], gu[:, 400:])
+        z = prism.gemm_fp8_blockscale(q2, s2, *w2)
+        return z, prism.token_logprobs(z, top=5)
+
+    eager = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream(device=DEV)
+    with torch.cuda.stream(side):
+        for x in xs:
+            step(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [step(x) for x in xs]
+    for rep in range(4):
+        for z, r in got:
+            z.fill_(float("nan"))
+            r.lse.fill_(float("nan"))
+        torch.randn((1000, 1000), device=DEV).sum()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for (z, r), (ze, re) in zip(got, eager):
+            assert torch.equal(z, ze)
+            for a, b in zip(r, re):
+                assert torch.equal(a, b)
+
+
+def test_refusals():
+    x = torch.randn((4, 256), device=DEV)
+    q, s = prism.quantize_blocks_fp8(x)
+    w, sw = prism.quantize_tiles_fp8(x)
+    with pytest.raises(TypeError):
+        prism.quantize_blocks_fp8(x.double())
+    with pytest.raises(ValueError):
+        prism.quantize_blocks_fp8(x.view(2, 2, 256))
+    with pytest.raises(ValueError, match="contiguous rows"):
+        prism.quantize_blocks_fp8(x.t())
+    with pytest.raises(ValueError, match="overlapping"):
+        prism.quantize_blocks_fp8(x.view(-1).as_strided((4, 256), (128, 1)))
+    with pytest.raises(ValueError, match="overlapping"):
+        prism.token_logprobs(x[:1].expand(4, 256))
+    with pytest.raises(prism.PrismError) as e:
+        prism.quantize_blocks_fp8(x[:, :40].contiguous())
+    assert e.value.status == -2
+    with pytest.raises(prism.PrismError) as e:
+        prism.quantize_blocks_fp8(x[:, 1:129])       # not 16-byte aligned
+    assert e.value.status == -2
+    with pytest.raises(ValueError, match="scale"):
+        prism.quantize_blocks_fp8(x, scale=torch.empty((4, 2), device=DEV))
+    with pytest.raises(TypeError):
+        prism.quantize_tiles_fp8(x, q=torch.empty((4, 256), dtype=torch.int8, device=DEV))
+    with pytest.raises(TypeError):
+        prism.swiglu_quantize_fp8(x, x.half())
+    with pytest.raises(ValueError):
+        prism.swiglu_quantize_fp8(x, x[:2])
+    with pytest.raises(ValueError, match="row stride"):
+        prism.swiglu_quantize_fp8(x, torch.randn((4, 512), device=DEV)[:, :256])
+    with pytest.raises(TypeError):
+        prism.gemm_fp8_blockscale(q.view(torch.int8), s, w, sw)
+    with pytest.raises(ValueError, match="s_a"):
+        prism.gemm_fp8_blockscale(q, s.t().contiguous(), w, sw)
+    with pytest.raises(ValueError, match="s_w"):
+        prism.gemm_fp8_blockscale(q, s, w, sw.view(2, 1))
+    with pytest.raises(ValueError):
+        prism.gemm_fp8_blockscale(q, s, w[:, :128].contiguous(), sw)
+    with pytest.raises(TypeError):
+        prism.gemm_fp8_blockscale(q, s, w, sw, out_dtype=torch.float64)
+    with pytest.raises(ValueError):
+        prism.gemm_fp8_blockscale(q, s, w, sw, y=torch.empty((4, 5), device=DEV))
+    z = torch.randn((2, 100), device=DEV)
+    with pytest.raises(TypeError):
+        prism.token_logprobs(z, torch.zeros((2, 1), dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        prism.token_logprobs(z, torch.zeros((3, 1), dtype=torch.int64, device=DEV))
+    with pytest.raises(ValueError):
+        prism.token_logprobs(z, torch.zeros((2,), dtype=torch.int64, device=DEV))
+    with pytest.raises(prism.PrismError):
+        prism.token_logprobs(z, top=33)
+    with pytest.raises(prism.PrismError):
+        prism.token_logprobs(torch.randn((2, 200000), device=DEV), top=3,
+                             workspace=torch.empty((8,), dtype=torch.uint8, device=DEV))
+
+
+def test_empty_batches():
+    q, s = prism.quantize_blocks_fp8(torch.empty((0, 256), device=DEV))
+    assert q.shape == (0, 256) and s.shape == (2, 0)
+    w, sw = prism.quantize_tiles_fp8(torch.randn((40, 256), device=DEV))
+    assert prism.gemm_fp8_blockscale(q, s, w, sw).shape == (0, 40)
+    assert prism.quantize_tiles_fp8(torch.empty((0, 256), device=DEV))[1].shape == (0, 2)
+    assert prism.swiglu_quantize_fp8(torch.empty((0, 32), device=DEV), torch.empty((0, 32), device=DEV))[0].shape == (0, 32)
+    r = prism.token_logprobs(torch.empty((0, 50), device=DEV), top=4)
+    assert r.lse.shape == (0,) and r.top_ids.shape == (0, 4)
