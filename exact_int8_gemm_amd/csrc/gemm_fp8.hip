@@ -20,9 +20,10 @@
 // registers: every e4m3 value and product is exact there, and the error is
 // that of fp32 sums (2-norm 1e-8), at half the matrix rate.
 //
-// Lane layout (both): lane l supplies row (A) or column (B) l % 16; its 32
-// codes of a block are the two 16-byte chunks l / 16 and l / 16 + 4.  Result
-// register r of lane l is row 4 (l / 16) + r, column l % 16.
+// Lane layout (both): lane l supplies row l % 16 of either operand; its 32
+// codes of a block are the two 16-byte chunks l / 16 and l / 16 + 4.  The
+// weights are the instructions' A operand, so result register r of lane l is
+// weight row 4 (l / 16) + r, activation row l % 16.
 #include "fp8_math.h"
 #include "lds_copy.h"
 
@@ -35,99 +36,612 @@ using fp8::kBlock;
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 
-// 32 codes of a lane: chunk l / 16 and chunk l / 16 + 4 of a 128-block.
-struct Frag {
-  v4i lo, hi;
+// Workgroup barrier that the compiler may not move memory accesses across.
+__device__ inline void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// s_waitcnt lgkmcnt(0), no wait on vmcnt or expcnt (gfx9 encoding).
+__device__ inline void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
+// v as a value the compiler knows nothing about: what is computed from it is
+// computed at each use, not held in registers over the loop.
+__device__ inline uint32_t fresh(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+__device__ inline float uniform(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
+// Workgroup b of n -> its place in a list of n tiles: each of the 8 XCDs, which
+// receive workgroups in turn, takes a contiguous range.
+__device__ inline int xcd_order(int b, int n) {
+  const int xcd = b % 8, base = n / 8, rem = n % 8;
+  return xcd * base + min(xcd, rem) + b / 8;
+}
+
+// Tile `id`: groups of 8 tile rows, column by column, so that neighbouring
+// tiles, which run together on an XCD, share operand panels in its L2.
+__device__ inline void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int kGroup = 8;
+  const int per_group = kGroup * tiles_n;
+  const int grp = id / per_group, first = grp * kGroup;
+  const int gm = min(tiles_m - first, kGroup);
+  const int in = id - grp * per_group;
+  tm = first + in % gm;
+  tn = in / gm;
+}
+
+// Codes of a lane to f16, eight consecutive ones per operand.
+__device__ inline fp8::v8h to_f16(const v4i c, int hi) {
+  fp8::v8h o;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * hi + d], 1.0f, false);
+    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * hi + d], 1.0f, true);
+    o[4 * d] = a[0];
+    o[4 * d + 1] = a[1];
+    o[4 * d + 2] = b[0];
+    o[4 * d + 3] = b[1];
+  }
+  return o;
+}
+
+// 16 x 16 tiles: a lane's chunks l / 16 and l / 16 + 4 of its row's block.
+struct Frag16 {
+  v4i c[2];
 };
 
 template <bool EXACT>
-struct Operand;
+struct Operand16;
 
 template <>
-struct Operand<false> {
+struct Operand16<false> {
   v8i v;
-  __device__ inline explicit Operand(const Frag& f)
-      : v{f.lo[0], f.lo[1], f.lo[2], f.lo[3], f.hi[0], f.hi[1], f.hi[2], f.hi[3]} {}
+  Operand16() = default;
+  __device__ inline explicit Operand16(const Frag16& f)
+      : v{f.c[0][0], f.c[0][1], f.c[0][2], f.c[0][3], f.c[1][0], f.c[1][1], f.c[1][2], f.c[1][3]} {}
 };
 
 template <>
-struct Operand<true> {
+struct Operand16<true> {
   fp8::v8h v[4];
-  __device__ inline explicit Operand(const Frag& f) {
+  Operand16() = default;
+  __device__ inline explicit Operand16(const Frag16& f) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t u = (uint32_t)(s < 2 ? f.lo[2 * s + h] : f.hi[2 * (s - 2) + h]);
-        const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false);
-        const auto b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true);
-        v[s][4 * h] = a[0];
-        v[s][4 * h + 1] = a[1];
-        v[s][4 * h + 2] = b[0];
-        v[s][4 * h + 3] = b[1];
-      }
-    }
+    for (int s = 0; s < 4; ++s) v[s] = to_f16(f.c[s / 2], s % 2);
   }
 };
 
-__device__ inline v4f block_sum(const Operand<false>& a, const Operand<false>& b) {
+__device__ inline v4f block_sum(const Operand16<false>& a, const Operand16<false>& b) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
 }
-__device__ inline v4f block_sum(const Operand<true>& a, const Operand<true>& b) {
+__device__ inline v4f block_sum(const Operand16<true>& a, const Operand16<true>& b) {
   v4f p{0, 0, 0, 0};
 #pragma unroll
   for (int s = 0; s < 4; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[s], b.v[s], p, 0, 0, 0);
   return p;
 }
 
-// One wave per 16 x 16 output tile, operands straight from global memory.
-template <typename OUT, bool EXACT>
-__global__ __launch_bounds__(256) void gemm_fp8_wave_kernel(const uint8_t* __restrict__ q,
-                                                            const float* __restrict__ s_a,
-                                                            const uint8_t* __restrict__ w,
-                                                            const float* __restrict__ s_w, OUT* __restrict__ y, int M,
-                                                            int N, int K, int tiles_n) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Few rows (M <= 16 MT): bound by reading the weights once.  A workgroup owns
+// 16 CB columns and its waves share out K: the chain over the blocks cannot be
+// split, but the blocks' sums can.  In rounds of WAVES x PER blocks, each wave
+// multiplies its PER blocks straight from global memory (a lane's operands are
+// two 16-byte loads per row tile and block; those of the next round are
+// issued before this one's are used) and leaves the sums in LDS with the
+// blocks' scales s_a s_w; after one barrier, threads fold the round's blocks
+// into their outputs in order.  Rows past RP (4 where M <= 4) are not stored.
+template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES, int PER>
+__global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_t* __restrict__ q,
+                                                                    const float* __restrict__ s_a,
+                                                                    const uint8_t* __restrict__ w,
+                                                                    const float* __restrict__ s_w,
+                                                                    OUT* __restrict__ y, int M, int N, int K) {
+  static_assert(RP == 16 || (RP == 4 && MT == 1), "rows kept of a row tile");
+  constexpr int NT = 64 * WAVES, C = WAVES * PER;
+  constexpr int kTile = 16 * RP;             // sums kept of a 16 x 16 tile
+  constexpr int kOut = MT * CB * kTile;      // outputs of the workgroup
+  constexpr int kPer = (kOut + NT - 1) / NT; // per thread
+  __shared__ __attribute__((aligned(16))) float lp[2][C][kOut];
+  __shared__ float ls[2][C][16 * MT];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r = lane & 15, g = lane >> 4;
-  const int64_t m0 = (int64_t)(blockIdx.x / (unsigned)tiles_n) * 16;
-  const int64_t n0 = ((int64_t)(blockIdx.x % (unsigned)tiles_n) * 4 + wave) * 16;
-  if (n0 >= N) return;
+  const int n0 = (int)blockIdx.x * 16 * CB;
   const int KB = (K + kBlock - 1) / kBlock;
-  const auto ra = make_rsrc(q + m0 * K, (M - m0) * K);
-  const auto rb = make_rsrc(w + n0 * K, (N - n0) * K);
-  auto load = [&](__amdgpu_buffer_rsrc_t rs, bool in, int b) {
-    Frag f;
-    const int k0 = b * kBlock + 16 * g, k1 = k0 + 64;
-    f.lo = __builtin_amdgcn_raw_buffer_load_b128(rs, in && k0 < K ? (uint32_t)(r * K + k0) : kOutOfRange, 0, 0);
-    f.hi = __builtin_amdgcn_raw_buffer_load_b128(rs, in && k1 < K ? (uint32_t)(r * K + k1) : kOutOfRange, 0, 0);
-    return f;
+  const auto rx = make_rsrc(q, (int64_t)M * K);
+  const auto rw = make_rsrc(w + (size_t)n0 * (size_t)K, (int64_t)(N - n0) * K);
+  const float* swp = s_w + (size_t)(n0 / kBlock) * (size_t)KB;
+
+  struct Round {
+    Frag16 x[PER][MT], w[PER][CB];
+    float sa[PER], sw[PER];  // lane l: the scales of row l (multiplied when used: here they would wait for all loads)
   };
-  v4f f{0, 0, 0, 0};
-  for (int b = 0; b < KB; ++b) {
-    const Operand<EXACT> a(load(ra, m0 + r < M, b)), c(load(rb, n0 + r < N, b));
-    const v4f p = block_sum(a, c);
-    const float sw = s_w[(n0 / kBlock) * KB + b];
+  // Rows past M or N read zeros (past their buffer's end), as do chunks past K.
+  auto load = [&](int b0, Round& d) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t m = m0 + 4 * g + i;
-      const float sa = m < M ? s_a[(int64_t)b * M + m] : 0.0f;
-      f[i] = __builtin_fmaf(p[i], sa * sw, f[i]);
+    for (int p = 0; p < PER; ++p) {
+      const int b = b0 + wave * PER + p;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = b * kBlock + 16 * g + 64 * h;
+        const bool in = k < K;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          d.x[p][i].c[h] = __builtin_amdgcn_raw_buffer_load_b128(
+              rx, in && 16 * i + r < M ? (uint32_t)((16 * i + r) * K + k) : kOutOfRange, 0, 0);
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+          d.w[p][j].c[h] = __builtin_amdgcn_raw_buffer_load_b128(
+              rw, in ? (uint32_t)((16 * j + r) * K + k) : kOutOfRange, 0, 0);
+      }
+      const int bb = b < KB ? b : KB - 1;  // blocks past K are not folded
+      d.sa[p] = s_a[(size_t)bb * (size_t)M + (lane < M ? lane : M - 1)];
+      d.sw[p] = swp[bb];
     }
+  };
+  auto multiply = [&](int buf, const Round& d) __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int bl = wave * PER + p;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const Operand16<EXACT> xo(d.x[p][i]);
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+          const v4f v = block_sum(Operand16<EXACT>(d.w[p][j]), xo);
+          if (r < RP) *reinterpret_cast<v4f*>(&lp[buf][bl][(i * CB + j) * kTile + (g * RP + r) * 4]) = v;
+        }
+      }
+      if (lane < 16 * MT) ls[buf][bl][lane] = d.sa[p] * d.sw[p];
+    }
+  };
+  float f[kPer];
+#pragma unroll
+  for (int o = 0; o < kPer; ++o) f[o] = 0.0f;
+  auto fold = [&](int buf, int count) __attribute__((always_inline)) {
+#pragma unroll
+    for (int o = 0; o < kPer; ++o) {
+      const int e = (int)threadIdx.x + NT * o;
+      if (e >= kOut) break;
+      const int m = 16 * (e / kTile / CB) + e / 4 % RP;
+      const float* pv = &lp[buf][0][e];
+      const float* sv = &ls[buf][0][m];
+      if (count == C) {
+#pragma unroll 8
+        for (int b = 0; b < C; ++b) f[o] = __builtin_fmaf(pv[b * kOut], sv[b * 16 * MT], f[o]);
+      } else {
+        for (int b = 0; b < count; ++b) f[o] = __builtin_fmaf(pv[b * kOut], sv[b * 16 * MT], f[o]);
+      }
+    }
+  };
+  Round cur, next;
+  load(0, cur);
+  int buf = 0;
+  for (int b0 = 0; b0 < KB; b0 += C) {
+    load(b0 + C, next);  // past K: zeros; behind a branch, the loads before it could not be awaited alone
+    multiply(buf, cur);
+    __syncthreads();  // also: every thread is done folding the round before last out of the other buffer
+    fold(buf, KB - b0 < C ? KB - b0 : C);
+    cur = next;
+    buf ^= 1;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + 4 * g + i;
-    if (m < M && n0 + r < N) y[m * N + n0 + r] = (OUT)f[i];
+  for (int o = 0; o < kPer; ++o) {
+    const int e = (int)threadIdx.x + NT * o;
+    if (e >= kOut) break;
+    const int t = e / kTile, m = 16 * (t / CB) + e / 4 % RP;
+    const int n = n0 + 16 * (t % CB) + 4 * (e % kTile / (4 * RP)) + e % 4;
+    if (m < M && n < N) y[(size_t)m * (size_t)N + (size_t)n] = (OUT)f[o];
   }
 }
 
+template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES, int PER>
+void launch_small(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
+                  hipStream_t st) {
+  gemm_fp8_small_kernel<OUT, EXACT, MT, RP, CB, WAVES, PER><<<(unsigned)((N + 16 * CB - 1) / (16 * CB)), 64 * WAVES, 0,
+                                                              st>>>(q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K);
+}
+
+// Waves and columns per workgroup by N: about 80 to 160 workgroups of eight
+// waves for narrow outputs, which are short of workgroups (MI355X, M = 1, us:
+// 2560 x 9728 8.4, 16 columns more 11.8; 5120 x 5120 7.3, 16 columns fewer 8.3),
+// four waves and 16 columns for wide ones (9728 x 2560 6.7, eight waves 8.0).
+template <typename OUT, bool EXACT>
+void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N,
+                       int K, hipStream_t st) {
+#define PRISM_FP8_SMALL(MT, RP)                                                                    \
+  if (N <= 3840) launch_small<OUT, EXACT, MT, RP, 1, 8, 1>(q, s_a, w, s_w, y, M, N, K, st);         \
+  else if (N <= 8192) launch_small<OUT, EXACT, MT, RP, 2, 8, 1>(q, s_a, w, s_w, y, M, N, K, st);    \
+  else launch_small<OUT, EXACT, MT, RP, 1, 4, 1>(q, s_a, w, s_w, y, M, N, K, st)
+  if (M <= 4) {
+    PRISM_FP8_SMALL(1, 4);
+  } else if (M <= 16) {
+    PRISM_FP8_SMALL(1, 16);
+  } else if (M <= 32) {
+    PRISM_FP8_SMALL(2, 16);
+  } else if constexpr (EXACT) {
+    PRISM_FP8_SMALL(4, 16);
+  }
+#undef PRISM_FP8_SMALL
+}
+
+// Four consecutive outputs of a row, rounded once each.
+template <typename OUT>
+struct alignas(4 * sizeof(OUT)) Out4 {
+  OUT v[4];
+};
+
+// LDS-tiled kernel.  One workgroup of 2 x WN waves owns BM = 32 TM rows by BN =
+// 16 TN WN columns and walks K one 128-block (a stage) at a time; a stage is
+// the block's BM + BN rows of 128 codes and the rows' scales, copied directly
+// into one of R LDS buffers.
+//
+// A lane holds four consecutive columns of one row of each 16 x 16 tile: its
+// row scale is one value per 16 rows, the fold one multiplication per 16 rows
+// and one fma per output, and y is written in pieces of four.  Frag row p of
+// column tile j is weight row 4 TN (p / 4) + 4 j + p % 4 of the wave's 16 TN,
+// which makes a lane's columns over its tiles consecutive.
+//
+// A wave keeps a stage's weight rows in registers and streams its TM row tiles
+// past them, each read two tiles ahead.  Each MFMA is followed by the fold of
+// the one kLag before it, whose result is then there without a wait.  The last
+// two row tiles are multiplied together, column tile by column tile, so that
+// each weight fragment's registers are free for the next stage's as early as
+// possible.
+//
+// Two barriers per stage hand parts of the buffer back as they are read: at
+// Q (before row tile QI) every wave has read the weights and the first QI + 2
+// row tiles, at P (before the last two row tiles) the rest; short tiles have P
+// only.  Behind each come the copies, into those parts, of the stage R later,
+// between MFMAs.  They are awaited about R - 1/2 stages later, by count
+// (vmcnt), so that a line that comes from HBM has that long to arrive (waits
+// taken away, the kernels take the same time).
+//
+// What bounds the 256 x 256 form, MI355X, M = N = K = 8192 (480-510 us, 2.2
+// PFLOP/s; 8192 x 5120 x 5120: 200 us, 2.1 PFLOP/s): the matrix cores are busy
+// 58% of the cycles at a clock that the power limit holds at 1.9 GHz; without
+// the copies it takes 423 us, without the LDS reads 416, without the folds
+// 405, without either barrier 465.  Times of these parts add up rather than
+// hide behind each other, because each costs clock.  Other forms measured and
+// not kept: 32 x 32 x 64 MFMAs (4% slower at 8192), all copies of a stage
+// issued together (265 against 225 us at 8192 x 5120 x 5120), one barrier per
+// stage (4% slower), 128 x 128 tiles of four waves (twice the copies: 560 us).
+template <int WN, int TM, int TN, int R>
+constexpr int kTileLds = R * ((32 * TM + 16 * TN * WN) * kBlock + 128 * WN * 4);  // R stages
+
+// The tile of BM rows from m0 and BN columns from n0.
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R>
+__device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, const uint8_t* __restrict__ q,
+                                                                const float* __restrict__ s_a,
+                                                                const uint8_t* __restrict__ w,
+                                                                const float* __restrict__ s_w, OUT* __restrict__ y,
+                                                                int M, int N, int K, int m0, int n0) {
+  constexpr int NW = 2 * WN;
+  constexpr int BM = 32 * TM, BN = 16 * TN * WN;
+  static_assert((TN == 2 || TN == 4) && BN % (8 * NW) == 0, "column tiles");
+  static_assert(TM % 2 == 0 && (NW == 8 || NW == 4), "pairs of row tiles, 4 or 8 waves");
+  static_assert(64 * NW >= BM, "one scale copy per wave covers the rows");
+  // 1 KiB copies (8 rows) per wave: V per pair of row tiles (64 rows), kB for
+  // the weights.
+  constexpr int V = 8 / NW, kB = BN / 8 / NW;
+  constexpr int QI = TM >= 6 ? 2 : 0;                  // Q stands before row tile QI (TM = 2: no Q)
+  constexpr bool HAS_Q = TM >= 4;
+  constexpr int kPairsQ = HAS_Q ? (QI + 2) / 2 : 0;    // pairs handed back at Q
+  constexpr int nQ = HAS_Q ? kB + V * kPairsQ : 0;     // copies behind Q: weights, then those pairs
+  constexpr int nP = 1 + (HAS_Q ? 0 : kB) + V * (TM / 2 - kPairsQ);  // behind P: scales, the rest
+  constexpr int kXBuf = BM * kBlock, kWBuf = BN * kBlock;
+  constexpr int kScales = 64 * NW;  // floats per stage
+  static_assert(R * (kXBuf + kWBuf + kScales * 4) == kTileLds<WN, TM, TN, R>, "LDS");
+  int8_t* const lx = lds;
+  int8_t* const lw = lds + R * kXBuf;
+  float* const lsa = reinterpret_cast<float*>(lds + R * (kXBuf + kWBuf));
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave / WN, wn = wave % WN;
+  const int r = lane & 15, g = lane >> 4;
+  const int KB = (K + kBlock - 1) / kBlock;
+
+  // 16-byte chunk c of row x lies at chunk c ^ swz(x): the 16 rows that 16
+  // neighbouring lanes read at one chunk then fall into 16 different 16-byte
+  // columns of a 256-byte window (two rows).
+  auto swz_a = [](int row) { return (row >> 1) & 7; };
+  auto swz_b = [](int row) { return ((row >> 1) & 1) | (((row >> (TN == 4 ? 4 : 3)) & 3) << 1); };
+  const v4i ra = tiled::dma::rsrc_words(q + (size_t)m0 * (size_t)K, (int64_t)min(M - m0, BM) * K);
+  const v4i rb = tiled::dma::rsrc_words(w + (size_t)n0 * (size_t)K, (int64_t)(N - n0) * K);
+  const uint32_t lx0 = tiled::dma::lds_addr(lx), lw0 = tiled::dma::lds_addr(lw);
+  const uint32_t lsa0 = tiled::dma::lds_addr(reinterpret_cast<const int8_t*>(lsa));
+  // Row group rho (8 rows) of a pair of row tiles: rows 8 (rho % 4) .. of the
+  // pair's 32 rows of wave row rho / 4.  This wave copies rho = wave + NW v.
+  // The swizzles repeat every 16 (weights: 64) rows, so a lane's source chunk
+  // is the same in all its activation copies (weights: of each parity).
+  const int arow = (wave >> 2) * 16 * TM + (wave & 3) * 8;  // + 16 TM v + 32 pair
+  const int brow = wave * 8;                                // + 8 NW i
+  const uint32_t ca = (uint32_t)(((lane & 7) ^ swz_a((wave & 3) * 8 + (lane >> 3))) * 16);
+  const uint32_t cb0 = (uint32_t)(((lane & 7) ^ swz_b(brow + (lane >> 3))) * 16);
+  const uint32_t cb1 = (uint32_t)(((lane & 7) ^ swz_b(brow + 8 * NW + (lane >> 3))) * 16);
+  const uint32_t xoff = (uint32_t)((lane >> 3) * K) + ca, woff = (uint32_t)((lane >> 3) * K);
+  // Rows past M or N lie past their buffer's end and chunks past K are sent
+  // there: both read zeros.
+  auto copy_x = [&](int c, int b, int buf) __attribute__((always_inline)) {  // c = V pair + v
+    const uint32_t ck = (uint32_t)b * kBlock;
+    const int row = arow + 16 * TM * (c % V) + 32 * (c / V);
+    const uint32_t in = fresh(xoff) + ((uint32_t)(row * K) + ck);
+    const uint32_t o = ca + ck < (uint32_t)K ? in : kOutOfRange;
+    tiled::dma::copy_to_lds(ra, lx0 + (uint32_t)(buf * kXBuf + row * kBlock), o);
+  };
+  auto copy_w = [&](int i, int b, int buf) __attribute__((always_inline)) {
+    const uint32_t ck = (uint32_t)b * kBlock;
+    const int row = brow + 8 * NW * i;
+    const uint32_t cb = NW == 4 && i % 2 == 1 ? cb1 : cb0;
+    const uint32_t in = fresh(woff) + cb + ((uint32_t)(row * K) + ck);
+    const uint32_t o = cb + ck < (uint32_t)K ? in : kOutOfRange;
+    tiled::dma::copy_to_lds(rb, lw0 + (uint32_t)(buf * kWBuf + row * kBlock), o);
+  };
+  auto copy_s = [&](int b, int buf) __attribute__((always_inline)) {
+    const int bb = b < KB ? b : KB - 1;
+    const v4i rs = tiled::dma::rsrc_words(s_a + (size_t)bb * (size_t)M + (size_t)m0,
+                                          b < KB ? (int64_t)min(M - m0, BM) * 4 : 0);
+    tiled::dma::copy4_to_lds(rs, lsa0 + (uint32_t)((buf * kScales + wave * 64) * 4), (uint32_t)(wave * 64 + lane) * 4u);
+  };
+  auto copy_behind_q = [&](int c, int b, int buf) __attribute__((always_inline)) {
+    if (c < kB) copy_w(c, b, buf);
+    else copy_x(c - kB, b, buf);
+  };
+  auto copy_behind_p = [&](int c, int b, int buf) __attribute__((always_inline)) {
+    if (c == 0) copy_s(b, buf);
+    else if (!HAS_Q && c <= kB) copy_w(c - 1, b, buf);
+    else copy_x(c - 1 - (HAS_Q ? 0 : kB) + V * kPairsQ, b, buf);
+  };
+
+  const int xrow = wm * TM * 16 + r;
+  const int wrow = wn * 16 * TN + 4 * TN * (r >> 2) + (r & 3);
+  const int xat = xrow * kBlock + ((g ^ swz_a(xrow)) * 16);
+  const int wat0 = wrow * kBlock + ((g ^ swz_b(wrow)) * 16);
+  auto read_x = [&](int buf, int i) __attribute__((always_inline)) {
+    const int8_t* p = lx + buf * kXBuf + i * 16 * kBlock;
+    return Frag16{*reinterpret_cast<const v4i*>(p + xat), *reinterpret_cast<const v4i*>(p + (xat ^ 64))};
+  };
+  auto read_w = [&](int buf, int j) __attribute__((always_inline)) {
+    const int8_t* p = lw + buf * kWBuf + j * 4 * kBlock;
+    const int wat = (int)fresh((uint32_t)wat0);
+    return Frag16{*reinterpret_cast<const v4i*>(p + wat), *reinterpret_cast<const v4i*>(p + (wat ^ 64))};
+  };
+  auto read_s = [&](int buf, int i) __attribute__((always_inline)) { return lsa[buf * kScales + xrow + 16 * i]; };
+  const int nb = min((n0 + wn * 16 * TN) / kBlock, (N - 1) / kBlock);
+  const float* swp = s_w + (size_t)nb * (size_t)KB;
+
+  // MFMA t of a stage: row tile tile(t) by column tile col(t).
+  constexpr int kT = TN * TM, kP = TN * (TM - 2), kQ = TN * QI;
+  constexpr int kPerP = (nP + 2 * TN - 1) / (2 * TN);                         // copies per MFMA
+  constexpr int kPerQ = HAS_Q ? (nQ + kP - kQ - 1) / (kP > kQ ? kP - kQ : 1) : 1;
+  constexpr int kLag = 3;
+  auto tile = [](int t) { return t < kP ? t / TN : TM - 2 + (t - kP) % 2; };
+  auto col = [](int t) { return t < kP ? t % TN : (t - kP) / 2; };
+  v4f f[kT], p[kLag];
+#pragma unroll
+  for (int t = 0; t < kT; ++t) f[t] = v4f{0, 0, 0, 0};
+#pragma unroll
+  for (int t = 0; t < kLag; ++t) p[t] = v4f{0, 0, 0, 0};
+  Frag16 x[2];
+  float sa[2];
+  float sw_next = swp[0];
+  float scp[2] = {0.0f, 0.0f};  // scales of the last two row tiles of the stage before
+  auto fold = [&](int i, int j, const v4f& pv, float sc) __attribute__((always_inline)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[TN * i + j][e] = __builtin_fmaf(pv[e], sc, f[TN * i + j][e]);
+  };
+
+  // Stage b in buffer buf, the next one in bufn (constants where R = 2).
+  auto stage = [&](int b, const int buf, const int bufn, const Frag16* wf, Frag16* wnext) __attribute__((always_inline)) {
+    // Weight scale, read a stage ahead (past a select, since a branch would
+    // split the loop body) and kept scalar.
+    const float sw = uniform(b < KB ? sw_next : 0.0f);
+    sw_next = swp[min(b + 1, KB - 1)];
+    Operand16<EXACT> wo[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) wo[j] = Operand16<EXACT>(wf[j]);
+    Frag16 xs[TM + 2];
+    float ss[TM + 2], sc[TM];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      xs[i] = x[i];
+      ss[i] = sa[i];
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      const int i = tile(t), j = col(t);
+      const v4f pn = block_sum(wo[j], Operand16<EXACT>(xs[i]));
+      __builtin_amdgcn_sched_barrier(0);
+      if (t == kP || (HAS_Q && t == kQ)) {
+        wait_lgkm0();  // this wave's reads of what is handed back
+        if (t == kP) tiled::dma::wait_vmcnt<(R - 2) * (nQ + nP) + (HAS_Q ? nQ + nP - 1 : 0)>();
+        else tiled::dma::wait_vmcnt<(R - 1) * (nQ + nP)>();
+        barrier();
+      }
+      if (t < kP && j == 0) {
+        xs[i + 2] = read_x(buf, i + 2);
+        ss[i + 2] = read_s(buf, i + 2);
+      }
+      if (t == kP || t == kP + TN) {
+        const int a = (t - kP) / TN;
+        x[a] = read_x(bufn, a);
+        sa[a] = read_s(bufn, a);
+      }
+      if (t >= kP && (t - kP) % 2 == 1) wnext[j] = read_w(bufn, j);
+      if (t >= kP) {
+#pragma unroll
+        for (int c = (t - kP) * kPerP; c < (t - kP + 1) * kPerP; ++c)
+          if (c < nP) copy_behind_p(c, b + R, buf);
+      } else if (HAS_Q && t >= kQ) {
+#pragma unroll
+        for (int c = (t - kQ) * kPerQ; c < (t - kQ + 1) * kPerQ; ++c)
+          if (c < nQ) copy_behind_q(c, b + R, buf);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      const int tp = (t + kT - kLag) % kT, ip = tile(tp);
+      if (t >= kLag && (t == kLag || (tp < kP ? tp % TN == 0 : tp - kP < 2))) sc[ip] = ss[ip] * sw;
+      fold(ip, col(tp), p[0], t >= kLag ? sc[ip] : scp[tp % 2]);
+#pragma unroll
+      for (int e = 0; e + 1 < kLag; ++e) p[e] = p[e + 1];
+      p[kLag - 1] = pn;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    scp[0] = ss[TM - 2] * sw;
+    scp[1] = ss[TM - 1] * sw;
+  };
+  static_assert(kLag < kT && kLag <= 2 * TN, "the folds left over are of the last two row tiles");
+
+  static_assert(R >= 2 && (R - 1) * (nQ + nP) < 64, "vmcnt range");
+#pragma unroll
+  for (int b = 0; b < R; ++b) {
+#pragma unroll
+    for (int c = 0; c < nQ; ++c) copy_behind_q(c, b, b);
+#pragma unroll
+    for (int c = 0; c < nP; ++c) copy_behind_p(c, b, b);
+  }
+  tiled::dma::wait_vmcnt<(R - 1) * (nQ + nP)>();
+  barrier();
+  Frag16 w0[TN], w1[TN];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x[i] = read_x(0, i);
+    sa[i] = read_s(0, i);
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j) w0[j] = read_w(0, j);
+  // Two stages per turn; a stage past K multiplies zeros by scales 0 and
+  // leaves f as it is (f starts at +0 and is never -0).
+  if constexpr (R == 2) {
+    for (int b = 0; b < KB; b += 2) {
+      stage(b, 0, 1, w0, w1);
+      stage(b + 1, 1, 0, w1, w0);
+    }
+  } else {
+    int b0 = 0, b1 = 1;
+    for (int b = 0; b < KB; b += 2) {
+      stage(b, b0, b1, w0, w1);
+      b0 = b1 + 1 == R ? 0 : b1 + 1;
+      stage(b + 1, b1, b0, w1, w0);
+      b1 = b0 + 1 == R ? 0 : b0 + 1;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kLag; ++t) fold(tile(kT - kLag + t), col(kT - kLag + t), p[t], scp[(kT - kLag + t) % 2]);
+  tiled::dma::wait_vmcnt<0>();  // no copy may land in LDS after the workgroup ends
+
+  // A lane's 16 columns n .. n + 15 of each of its rows.
+  const int n = n0 + wn * 16 * TN + 4 * TN * g;
+  const bool wide = N % 4 == 0 && reinterpret_cast<uintptr_t>(y) % sizeof(Out4<OUT>) == 0;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = m0 + xrow + 16 * i;
+    if (m >= M) continue;
+    OUT* yr = y + (size_t)m * (size_t)N;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if (wide) {
+        if (n + 4 * j < N) {
+          Out4<OUT> o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.v[e] = (OUT)f[TN * i + j][e];
+          *reinterpret_cast<Out4<OUT>*>(yr + n + 4 * j) = o;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + 4 * j + e < N) yr[n + 4 * j + e] = (OUT)f[TN * i + j][e];
+      }
+    }
+  }
+}
+
+// One workgroup per tile, the last tiles in smaller ones: `full` tiles of 32 TM
+// rows, then the others cut into TM / TAIL pieces of 32 TAIL rows each.  A
+// launch whose tiles do not fill its last round of compute units takes a whole
+// round for them otherwise (2048 x 17408: 544 tiles on 256 CUs are 3 rounds,
+// 512 and 32 x 4 quarters little more than 2).
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int RT, int OCC>
+__global__ __launch_bounds__(128 * WN, OCC) void gemm_fp8_tile_kernel(const uint8_t* __restrict__ q,
+                                                                      const float* __restrict__ s_a,
+                                                                      const uint8_t* __restrict__ w,
+                                                                      const float* __restrict__ s_w,
+                                                                      OUT* __restrict__ y, int M, int N, int K,
+                                                                      int tiles_m, int tiles_n, int full) {
+  constexpr int kLds = TAIL < TM && kTileLds<WN, TAIL, TN, RT> > kTileLds<WN, TM, TN, R>
+                           ? kTileLds<WN, TAIL, TN, RT>
+                           : kTileLds<WN, TM, TN, R>;
+  static_assert(kLds <= 160 * 1024 / OCC, "LDS");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kLds];
+  const int b = (int)blockIdx.x;
+  if (b < full) {
+    int tm, tn;
+    tile_of(xcd_order(b, full), tiles_m, tiles_n, tm, tn);
+    tile_body<OUT, EXACT, WN, TM, TN, R>(lds, q, s_a, w, s_w, y, M, N, K, tm * 32 * TM, tn * 16 * TN * WN);
+  } else if constexpr (TAIL < TM) {
+    constexpr int S = TM / TAIL;
+    int tm, tn;
+    const int id = xcd_order(b - full, (int)gridDim.x - full);
+    tile_of(full + id / S, tiles_m, tiles_n, tm, tn);
+    const int m0 = tm * 32 * TM + id % S * 32 * TAIL;
+    if (m0 < M) tile_body<OUT, EXACT, WN, TAIL, TN, RT>(lds, q, s_a, w, s_w, y, M, N, K, m0, tn * 16 * TN * WN);
+  }
+}
+
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int RT, int OCC>
+void launch_tile(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
+                 int full, hipStream_t st) {
+  constexpr int BM = 32 * TM, BN = 16 * TN * WN;
+  const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n;
+  const int grid = full + (tiles - full) * (TM / TAIL);
+  gemm_fp8_tile_kernel<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC><<<(unsigned)grid, 128 * WN, 0, st>>>(
+      q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K, tiles_m, tiles_n, full);
+}
+
+// Number of compute units that the choices below count with (MI355X).
+constexpr int kCus = 256;
+
+// Kernel for (M, N), fitted on MI355X with inputs rotated through 0.6 GB (us
+// below; every choice gives the same bits):
+//  * small kernel: M <= 8; up to 16 rows where N <= 16384 (17408 x 5120, M =
+//    16: 64 x 64 tiles 20.6 against 24.0), up to 32 rows where N <= 6144 (5120
+//    x 5120, M = 32: 11.9 against 15.0), for an fp32 y up to 64 rows there
+//    (5120 x 5120, M = 64: 18.5 against 22.5);
+//  * 64 x 64 tiles while they fit the CUs at once (128 x 5120 x 5120: 15.3,
+//    64 x 128 tiles 18.1), for an fp32 y, which is bound by the MFMAs and
+//    conversions of a wave, up to five per CU (512 x 9728 x 2560: 38 against 43
+//    with 128 x 128; 2048 x 5120 x 5120 the other way, 119 against 142);
+//  * 16-bit y: 64 x 128 tiles while they fit the CUs at once (500 x 2560 x
+//    9680: 34.9, 64 x 64 40.6, 128 x 128 47);
+//  * else the smallest estimate of 128 x 128, 192 x 256 and 256 x 256 tiles:
+//    rounds of the CUs (two workgroups each for 128 x 128) times a round's
+//    cost relative to 256 x 256; 256 x 256 tiles that fill at most half of
+//    their last round are cut in two there, for 0.6 of a round (8192 x 5120 x
+//    5120: 221 -> 200).
 template <typename OUT, bool EXACT>
 int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
            hipStream_t st) {
-  const int tiles_n = (N + 63) / 64;
-  const int64_t grid = (int64_t)((M + 15) / 16) * tiles_n;
-  gemm_fp8_wave_kernel<OUT, EXACT>
-      <<<(unsigned)grid, 256, 0, st>>>(q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K, tiles_n);
+  auto tiles = [&](int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+#define PRISM_FP8_TILE(WN, TM, TN, R, TAIL, RT, OCC, FULL) \
+  launch_tile<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC>(q, s_a, w, s_w, y, M, N, K, (int)(FULL), st)
+  if (M <= 8 || (M <= 16 && N <= 16384) || (M <= (EXACT ? 64 : 32) && N <= 6144)) {
+    launch_small_rows<OUT, EXACT>(q, s_a, w, s_w, y, M, N, K, st);
+  } else if (tiles(64, 64) <= (EXACT ? 5 : 1) * kCus) {
+    PRISM_FP8_TILE(2, 2, 2, 3, 2, 3, 3, tiles(64, 64));
+  } else if constexpr (EXACT) {
+    PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, tiles(128, 128));
+  } else if (tiles(64, 128) <= kCus) {
+    PRISM_FP8_TILE(4, 2, 2, 3, 2, 3, 2, tiles(64, 128));
+  } else {
+    const int64_t t256 = tiles(256, 256), last = t256 % kCus;
+    const float c256 = (float)(t256 / kCus) + (last == 0 ? 0.0f : 2 * last <= kCus ? 0.6f : 1.0f);
+    const float c192 = 0.8f * (float)((tiles(192, 256) + kCus - 1) / kCus);
+    const float c128 = 0.64f * (float)((tiles(128, 128) + 2 * kCus - 1) / (2 * kCus));
+    if (c128 < c192 && c128 < c256) PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, tiles(128, 128));
+    else if (c192 < c256) PRISM_FP8_TILE(4, 6, 4, 2, 6, 2, 1, tiles(192, 256));
+    else PRISM_FP8_TILE(4, 8, 4, 2, 4, 2, 1, 2 * last <= kCus ? t256 - last : t256);
+  }
+#undef PRISM_FP8_TILE
   return launch_status();
 }
 

@@ -335,7 +335,7 @@ int64_t token_logprobs_bytes(int64_t M, int64_t V, int top) {
   return chunks > 1 ? M * chunks * (8 * (int64_t)top + (int64_t)sizeof(Stats)) : 0;
 }
 
-bool token_logprobs_grid_fits(int64_t M, int64_t V) { return M * ((V + kChunk - 1) / kChunk) <= 0x7fffffff; }
+int64_t token_logprobs_groups(int64_t M, int64_t V) { return M * ((V + kChunk - 1) / kChunk); }
 
 int launch_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t ntok, int top,
                           float* lp, float* lse, float* ent, int64_t* top_ids, float* top_lp, void* ws, int64_t M,

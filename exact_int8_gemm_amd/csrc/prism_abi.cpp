@@ -69,6 +69,9 @@ int check_gemm(const void* q, const void* s_a, const void* w, const void* scale_
   return PRISM_OK;
 }
 
+// Most workgroups of 256 threads in a launch (a grid has fewer than 2^32 threads).
+constexpr int64_t kMaxGroups256 = UINT32_MAX / 256;
+
 bool known_type(int t) { return t == PRISM_TYPE_F32 || t == PRISM_TYPE_F16 || t == PRISM_TYPE_BF16; }
 int64_t type_size(int t) { return t == PRISM_TYPE_F32 ? 4 : 2; }
 
@@ -84,7 +87,7 @@ int check_fp8_quant(const void* x, const void* x2, int type, int64_t ld, const v
   }
   if (K == 0 || K > PRISM_K_MAX || M > INT_MAX || ld < K || ld > INT64_MAX / 4 / M) return PRISM_ERR_INVALID_ARG;
   if (!x || !x2 || !q || !scale) return PRISM_ERR_INVALID_ARG;
-  if ((M + group_rows - 1) / group_rows * ((K + 127) / 128) > INT_MAX) return PRISM_ERR_INVALID_ARG;  // grid size
+  if ((M + group_rows - 1) / group_rows * ((K + 127) / 128) > kMaxGroups256) return PRISM_ERR_INVALID_ARG;  // grid size
   if (K % 16 != 0 || !aligned(x, 16) || !aligned(x2, 16) || ld * type_size(type) % 16 != 0 || !aligned(q, 16) ||
       !aligned(scale, 4))
     return PRISM_ERR_ALIGNMENT;
@@ -380,7 +383,7 @@ int prism_token_logprobs(const void* logits, int type, int64_t ld, const int64_t
     return PRISM_ERR_INVALID_ARG;
   const int64_t need = prism::token_logprobs_bytes(M, V, top);
   if (need > 0 && (!workspace || workspace_bytes < need)) return PRISM_ERR_INVALID_ARG;
-  if (!prism::token_logprobs_grid_fits(M, V)) return PRISM_ERR_INVALID_ARG;
+  if (prism::token_logprobs_groups(M, V) > kMaxGroups256) return PRISM_ERR_INVALID_ARG;  // grid size
   if (!aligned(logits, type_size(type)) || !aligned(tokens, 8) || !aligned(logprobs, 4) || !aligned(lse, 4) ||
       !aligned(entropy, 4) || !aligned(top_ids, 8) || !aligned(top_logprobs, 4) || !aligned(workspace, 8))
     return PRISM_ERR_ALIGNMENT;
