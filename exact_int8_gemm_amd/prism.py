@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -344,6 +345,25 @@ def _blocks(n):
     return (n + FP8_BLOCK - 1) // FP8_BLOCK
 
 
+def _launch(fn, dev, *args):
+    """fn(*args, the current stream of dev) with dev the current device; raises on a status."""
+    if torch.cuda.current_device() == dev.index:
+        # the raw handle, without a Stream object around it (2 us of a decode call's 8)
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status:
+        _check(status)
+
+
+def _is(t, name, dtype, shape, dev):
+    """_need's checks at once; _need only says which one failed."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape, dev)
+
+
 def _rows(x, name):
     """A 2-D float tensor on the GPU with contiguous rows (any row stride >= the row) -> (device, rows, cols, stride)."""
     dev = _gpu(x, name)
@@ -352,19 +372,25 @@ def _rows(x, name):
     if x.dtype not in TYPES:
         raise TypeError("%s must be float32, float16 or bfloat16, got %s" % (name, x.dtype))
     rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    ld, inner = x.stride()
+    if cols > 1 and inner != 1:
         raise ValueError("%s must have contiguous rows" % name)
-    # the stride of a single row is never used and may be anything
-    ld = x.stride(0) if rows > 1 else cols
-    if rows > 1 and ld < cols:
+    if rows <= 1:
+        ld = cols  # the stride of a single row is never used and may be anything
+    elif ld < cols:
         raise ValueError("%s has overlapping rows (row stride %d, %d columns)" % (name, ld, cols))
     return dev, rows, cols, ld
 
 
-def _fp8_outputs(q, scale, M, K, scale_shape, dev):
-    q = torch.empty((M, K), dtype=FP8, device=dev) if q is None else _need(q, "q", FP8, (M, K), dev)
-    scale = (torch.empty(scale_shape, dtype=torch.float32, device=dev) if scale is None
-             else _need(scale, "scale", torch.float32, scale_shape, dev))
+def _fp8_outputs(x, q, scale, scale_shape, dev):
+    if q is None:
+        q = torch.empty(x.shape, dtype=FP8, device=dev)
+    else:
+        _is(q, "q", FP8, x.shape, dev)
+    if scale is None:
+        scale = torch.empty(scale_shape, dtype=torch.float32, device=dev)
+    else:
+        _is(scale, "scale", torch.float32, scale_shape, dev)
     return q, scale
 
 
@@ -372,9 +398,8 @@ def quantize_blocks_fp8(x, q=None, scale=None):
     """x float32/float16/bfloat16 [M, K] on the GPU (rows may be strided) -> (q float8_e4m3fn [M, K],
     scale float32 [ceil(K/128), M]): one scale per 128 consecutive values of a row."""
     dev, M, K, ld = _rows(x, "x")
-    q, scale = _fp8_outputs(q, scale, M, K, (_blocks(K), M), dev)
-    with torch.cuda.device(dev):
-        _check(lib().prism_quantize_blocks_fp8(_ptr(x), TYPES[x.dtype], ld, _ptr(q), _ptr(scale), M, K, _stream(dev)))
+    q, scale = _fp8_outputs(x, q, scale, (_blocks(K), M), dev)
+    _launch(lib().prism_quantize_blocks_fp8, dev, x.data_ptr(), TYPES[x.dtype], ld, q.data_ptr(), scale.data_ptr(), M, K)
     return q, scale
 
 
@@ -382,9 +407,8 @@ def quantize_tiles_fp8(w, q=None, scale=None):
     """w float32/float16/bfloat16 [N, K] on the GPU (rows may be strided) -> (q float8_e4m3fn [N, K],
     scale float32 [ceil(N/128), ceil(K/128)]): one scale per 128 x 128 tile."""
     dev, N, K, ld = _rows(w, "w")
-    q, scale = _fp8_outputs(q, scale, N, K, (_blocks(N), _blocks(K)), dev)
-    with torch.cuda.device(dev):
-        _check(lib().prism_quantize_tiles_fp8(_ptr(w), TYPES[w.dtype], ld, _ptr(q), _ptr(scale), N, K, _stream(dev)))
+    q, scale = _fp8_outputs(w, q, scale, (_blocks(N), _blocks(K)), dev)
+    _launch(lib().prism_quantize_tiles_fp8, dev, w.data_ptr(), TYPES[w.dtype], ld, q.data_ptr(), scale.data_ptr(), N, K)
     return q, scale
 
 
@@ -401,10 +425,9 @@ def swiglu_quantize_fp8(gate, up, q=None, scale=None):
         raise ValueError("up must have shape %s, got %s" % ((M, K), (M2, K2)))
     if ld2 != ld:
         raise ValueError("gate and up must have the same row stride, got %d and %d" % (ld, ld2))
-    q, scale = _fp8_outputs(q, scale, M, K, (_blocks(K), M), dev)
-    with torch.cuda.device(dev):
-        _check(lib().prism_swiglu_quantize_fp8(_ptr(gate), _ptr(up), TYPES[gate.dtype], ld, _ptr(q), _ptr(scale), M, K,
-                                               _stream(dev)))
+    q, scale = _fp8_outputs(gate, q, scale, (_blocks(K), M), dev)
+    _launch(lib().prism_swiglu_quantize_fp8, dev, gate.data_ptr(), up.data_ptr(), TYPES[gate.dtype], ld, q.data_ptr(),
+            scale.data_ptr(), M, K)
     return q, scale
 
 
@@ -416,17 +439,20 @@ def gemm_fp8_blockscale(q, s_a, w, s_w, y=None, out_dtype=torch.float32):
         raise ValueError("q and w must be 2-D")
     M, K = q.shape
     N = w.shape[0]
-    _need(q, "q", FP8, (M, K), dev)
-    _need(s_a, "s_a", torch.float32, (_blocks(K), M), dev)
-    _need(w, "w", FP8, (N, K), dev)
-    _need(s_w, "s_w", torch.float32, (_blocks(N), _blocks(K)), dev)
+    kb = _blocks(K)
+    _is(q, "q", FP8, (M, K), dev)
+    _is(s_a, "s_a", torch.float32, (kb, M), dev)
+    _is(w, "w", FP8, (N, K), dev)
+    _is(s_w, "s_w", torch.float32, (_blocks(N), kb), dev)
     dtype = out_dtype if y is None else getattr(y, "dtype", None)
     if dtype not in TYPES:
         raise TypeError("y must be float32, float16 or bfloat16, got %s" % (dtype,))
-    y = torch.empty((M, N), dtype=dtype, device=dev) if y is None else _need(y, "y", dtype, (M, N), dev)
-    with torch.cuda.device(dev):
-        _check(lib().prism_gemm_fp8_blockscale(_ptr(q), _ptr(s_a), _ptr(w), _ptr(s_w), _ptr(y), TYPES[dtype], M, N, K,
-                                               _stream(dev)))
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+    else:
+        _is(y, "y", dtype, (M, N), dev)
+    _launch(lib().prism_gemm_fp8_blockscale, dev, q.data_ptr(), s_a.data_ptr(), w.data_ptr(), s_w.data_ptr(),
+            y.data_ptr(), TYPES[dtype], M, N, K)
     return y
 
 
@@ -447,26 +473,27 @@ def token_logprobs(logits, tokens=None, top=0, workspace=None):
         if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
             raise ValueError("tokens must be a 2-D tensor")
         T = tokens.shape[1]
-        _need(tokens, "tokens", torch.int64, (M, T), dev)
+        _is(tokens, "tokens", torch.int64, (M, T), dev)
     top = int(top)
     need = token_logprobs_workspace(M, V, top)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     else:
-        _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+        _is(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     r = TokenLogprobs(torch.empty((M, T), dtype=torch.float32, device=dev),
                       torch.empty((M,), dtype=torch.float32, device=dev),
                       torch.empty((M,), dtype=torch.float32, device=dev),
                       torch.empty((M, top), dtype=torch.int64, device=dev),
                       torch.empty((M, top), dtype=torch.float32, device=dev))
-    with torch.cuda.device(dev):
-        _check(lib().prism_token_logprobs(_ptr(logits), TYPES[logits.dtype], ld, _ptr(tokens), T, top,
-                                          _ptr(r.logprobs), _ptr(r.lse), _ptr(r.entropy), _ptr(r.top_ids),
-                                          _ptr(r.top_logprobs), _ptr(workspace),
-                                          0 if workspace is None else workspace.numel(), M, V, _stream(dev)))
+    _launch(lib().prism_token_logprobs, dev, logits.data_ptr(), TYPES[logits.dtype], ld,
+            tokens.data_ptr() if T else None, T, top, r.logprobs.data_ptr(), r.lse.data_ptr(), r.entropy.data_ptr(),
+            r.top_ids.data_ptr(), r.top_logprobs.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel(), M, V)
     return r
 
 
+@functools.lru_cache(maxsize=256)
 def token_logprobs_workspace(M, V, top):
     """Bytes of scratch memory that token_logprobs needs for these sizes (0: none)."""
     n = ctypes.c_int64(0)
