@@ -7,34 +7,34 @@
 //   lse = m + log S, logprob(t) = (z_t - m) - log S, entropy = log S - W / S.
 // Both terms of the entropy are >= 0, so nothing cancels.  m, S and W are
 // fp32; exp is one v_exp_f32 of (z - m) log2(e), whose error (|z - m| 2^-24
-// relative) is largest where the term itself vanishes.  (z log2(e) - m log2(e)
-// as one fma would save an instruction and be off by |z| 2^-24 in every term.)
+// relative) is largest where the term itself vanishes.
 //
 // The vocabulary axis is cut into chunks of kChunk values whatever M is, one
-// workgroup each, so a row's sums are always added in the same order.  A chunk
-// is read once and stays in registers: maximum, sums, and its `top` largest
-// values; a second kernel joins the chunks of a row.
+// wave each, so a row's sums are always added in the same order.  A chunk is
+// read once and stays in registers: maximum, sums, and its `top` largest
+// values; a second kernel joins the chunks of a row.  Waves do not wait for
+// each other and stay small: 56 registers, for 8 waves a SIMD.  2048 x 100003
+// bf16, top 8: 98 to 108 us (410 MB: 81 us at a large copy's rate) and 7 us for
+// the join.  With four waves and five barriers to each 8192 values, which left
+// the vector units idle 40% of the time, it took 143 us.  What bounds it now is
+// issue: per value an exp at a quarter of the rate and six other instructions.
 //
-// Top values: every thread's maximum goes to LDS; lane l takes the maximum
-// of the threads l, l + 64, ..., and the top-th largest of these 64 group
-// maxima is a value that at least `top` values of the chunk reach.  Only
-// values that reach it (usually a few more than `top`) are collected and
-// ranked, by value and then by index, as one 64-bit key each.  When too many
-// values tie there (a chunk masked to one finite value), the larger ones are
-// ranked and the tied ones marked in a bit per value, of which the first are
-// taken.
-//
+// Top values: a bisection finds a value t that at least `top` of the 64 lanes'
+// maxima reach, and often no more.  The values of those lanes alone are looked
+// at (of all lanes: 144 us instead of 108); the ones of at least t (a few more than `top`) are ranked, by value and
+// then by index, as one 64-bit key each.  When too many values tie at t (a
+// chunk masked to one finite value), the larger ones are ranked and the tied
+// ones marked in a bit per value, of which the first are taken.
 #include "../../include/prism.h"
 #include "prism_internal.h"
 
 namespace prism {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kPerThread = 32;
-constexpr int kChunk = kThreads * kPerThread;
-constexpr int kCand = 512;  // candidates ranked at once
-constexpr int kJoinThreads = 256;
+constexpr int kPerLane = 64;
+constexpr int kChunk = 64 * kPerLane;
+constexpr int kCand = 128;  // candidates of a chunk ranked at once
+constexpr int kHold = 16;   // lanes whose values are held in LDS at once
 constexpr int kJoinCand = 1024;
 constexpr float kLowest = -3.402823466e+38f;
 constexpr float kLog2E = 0x1.715476p+0f, kLn2 = 0x1.62e430p-1f;
@@ -42,6 +42,7 @@ constexpr float kNegInf = -__builtin_inff();
 // Lowest exponent of 2 taken: 2^-200 is 0 in fp32, and unlike -inf it can be
 // multiplied by that.
 constexpr float kFloor = -200.0f;
+constexpr float kLargest = 1e30f;
 
 struct Stats {
   float m, S, W;
@@ -49,20 +50,34 @@ struct Stats {
 
 // Keys order values first, then lower indices; 0 is below every key of a
 // value above -inf.  + 0.0f makes -0 equal to 0.
-__device__ inline uint64_t key_of(float v, uint32_t index) {
+__device__ inline uint32_t order_of(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
-  const uint32_t o = (b >> 31) ? ~b : (b | 0x80000000u);
-  return ((uint64_t)o << 32) | (uint32_t)~index;
+  return (b >> 31) ? ~b : (b | 0x80000000u);
 }
-__device__ inline float value_of(uint64_t key) {
-  const uint32_t o = (uint32_t)(key >> 32);
+__device__ inline float of_order(uint32_t o) {
   return __builtin_bit_cast(float, (o >> 31) ? (o & 0x7fffffffu) : ~o);
 }
+__device__ inline uint64_t key_of(float v, uint32_t index) {
+  return ((uint64_t)order_of(v) << 32) | (uint32_t)~index;
+}
+__device__ inline float value_of(uint64_t key) { return of_order((uint32_t)(key >> 32)); }
 __device__ inline uint32_t index_of(uint64_t key) { return ~(uint32_t)key; }
 
 template <typename T>
 __device__ inline float to_float(T v) {
   return (float)v;
+}
+
+// Value e of 16 bytes of values, as fp32; the last argument names their type.
+__device__ inline float value_at(const v4i p, int e, const float*) {
+  return __builtin_bit_cast(float, (uint32_t)p[e]);
+}
+__device__ inline float value_at(const v4i p, int e, const __bf16*) {
+  const uint32_t w = (uint32_t)p[e / 2];
+  return __builtin_bit_cast(float, e % 2 ? w & 0xffff0000u : w << 16);
+}
+__device__ inline float value_at(const v4i p, int e, const _Float16*) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)((uint32_t)p[e / 2] >> (e % 2 * 16)));
 }
 
 // m = -inf (nothing in the row or chunk) as the base of z - m.
@@ -96,7 +111,7 @@ __device__ inline float wave_reduce(float v, float neutral, F op) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 __device__ inline float wave_max(float v) {
-  return wave_reduce(v, kNegInf, [](float a, float b) { return fmaxf(a, b); });
+  return wave_reduce(v, kNegInf, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
 }
 __device__ inline float wave_min(float v) {
   return wave_reduce(v, -kNegInf, [](float a, float b) { return fminf(a, b); });
@@ -105,14 +120,26 @@ __device__ inline float wave_sum(float v) {
   return wave_reduce(v, 0.0f, [](float a, float b) { return a + b; });
 }
 
-// The top-th largest of the lanes' values (top <= 64): the least value that
-// fewer than `top` lanes exceed.
-__device__ inline float kth_of_wave(float g, int top) {
-  int above = 0;
-#pragma unroll 16
-  for (int i = 0; i < 64; ++i)
-    above += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, g), i)) > g ? 1 : 0;
-  return wave_min(above < top ? g : -kNegInf);
+// A value that at least `top` (<= 64) of the lanes' values reach, and often no
+// more of them: halvings of the ordered bit patterns between the values'
+// minimum and maximum.
+__device__ inline float kth_of_wave(float g, float largest, int top) {
+  const uint32_t o = order_of(g);
+  uint32_t lo = order_of(wave_min(g)), hi = order_of(largest) + 1;
+  for (int i = 0; i < 16 && hi - lo > 1; ++i) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int n = __popcll(__ballot(o >= mid));
+    if (n >= top) lo = mid;
+    else hi = mid;
+    if (n == top) break;
+  }
+  return of_order(__builtin_amdgcn_readfirstlane(lo));
+}
+
+// Orders this wave's LDS accesses: what its lanes wrote before is read after.
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 template <int NT>
@@ -131,7 +158,7 @@ __device__ inline uint64_t block_max_key(uint64_t v, uint64_t* lds) {
 // The n distinct keys in LDS: those of rank < top go to out[rank].
 template <int NT>
 __device__ inline void rank_keys(const uint64_t* keys, int n, int top, uint64_t* out) {
-  for (int i = threadIdx.x; i < n; i += NT) {
+  for (int i = threadIdx.x % NT; i < n; i += NT) {
     const uint64_t k = keys[i];
     int rank = 0;
 #pragma unroll 8
@@ -151,17 +178,18 @@ __device__ inline void write_row(const T* z, int64_t V, int64_t row, const Stats
   const float base = base_of(st.m);
   const float ls = logf(st.S);
   const float nan = __builtin_nanf("");
-  if (threadIdx.x == 0) {
+  const int tid = (int)(threadIdx.x % NT);
+  if (tid == 0) {
     if (lse) lse[row] = bad ? nan : empty ? kNegInf : base + ls;
     if (ent) ent[row] = bad ? nan : empty ? 0.0f : ls - st.W * kLn2 / st.S;
   }
-  for (int64_t i = threadIdx.x; i < ntok; i += NT) {
+  for (int64_t i = tid; i < ntok; i += NT) {
     const int64_t t = tokens[row * ntok + i];
     float r = nan;
     if (t >= 0 && t < V && !bad) r = empty ? kNegInf : (to_float(z[t]) - base) - ls;
     lp[row * ntok + i] = r;
   }
-  for (int i = threadIdx.x; i < top; i += NT) {
+  for (int i = tid; i < top; i += NT) {
     const uint64_t k = keys[i];
     float r = kNegInf;
     if (k != 0 && !empty && !bad) r = (value_of(k) - base) - ls;
@@ -170,130 +198,139 @@ __device__ inline void write_row(const T* z, int64_t V, int64_t row, const Stats
   }
 }
 
-// One chunk of one row: statistics and sorted top keys into stats[row][chunk]
-// and keys[row][chunk][top]; or, if the row is one chunk, the row's results.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(
-    const T* __restrict__ logits, int64_t ld, int64_t V, int chunks, int top, Stats* __restrict__ stats,
-    uint64_t* __restrict__ keys, const int64_t* __restrict__ tokens, int64_t ntok, float* __restrict__ lp,
-    float* __restrict__ lse, float* __restrict__ ent, int64_t* __restrict__ top_ids, float* __restrict__ top_lp) {
+// Chunk u % chunks of row u / chunks, u = this wave: statistics and sorted top
+// keys into stats[u] and keys[u][top]; or, if a row is one chunk, the row's
+// results.
+template <typename T, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
+    const T* __restrict__ logits, int64_t ld, int64_t V, unsigned total, int chunks, int top,
+    Stats* __restrict__ stats, uint64_t* __restrict__ keys, const int64_t* __restrict__ tokens, int64_t ntok,
+    float* __restrict__ lp, float* __restrict__ lse, float* __restrict__ ent, int64_t* __restrict__ top_ids,
+    float* __restrict__ top_lp) {
   constexpr int kVec = 16 / (int)sizeof(T);
-  constexpr int kIter = kPerThread / kVec;
-  constexpr int kWaves = kThreads / 64;
-  constexpr int kGroups = kPerThread / 8;
-  __shared__ float tmax[kThreads];
-  __shared__ float redS[kWaves], redW[kWaves];
-  __shared__ float lthr;
-  __shared__ uint64_t redk[kWaves];
-  __shared__ uint64_t cand[kCand];
-  __shared__ uint64_t best[PRISM_TOP_MAX];
-  __shared__ uint32_t tied[kChunk / 32];
-  __shared__ int ncand;
-  const int64_t row = blockIdx.x / (unsigned)chunks;
-  const int chunk = (int)(blockIdx.x % (unsigned)chunks);
-  const int64_t base = (int64_t)chunk * kChunk;
-  const T* z = logits + row * ld;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int kIter = kPerLane / kVec;
+  constexpr int kRow = kPerLane * (int)sizeof(T) + 16;  // 16 more bytes against bank conflicts
+  __shared__ __attribute__((aligned(16))) uint8_t lheld[WAVES][kHold * kRow];
+  __shared__ uint64_t lcand[WAVES][kCand];
+  __shared__ uint64_t lbest[WAVES][PRISM_TOP_MAX];
+  __shared__ uint32_t ltied[WAVES][kChunk / 32];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const unsigned u = blockIdx.x * WAVES + (unsigned)wave;
+  if (u >= total) return;  // no barrier below
+  uint8_t* held = lheld[wave];
+  uint64_t* cand = lcand[wave];
+  uint64_t* best = lbest[wave];
+  uint32_t* tied = ltied[wave];
+  const int64_t row = u / (unsigned)chunks;
+  const int64_t base = (int64_t)(u % (unsigned)chunks) * kChunk;
+  const T* z = logits + row * ld + base;
 
-  // Value i of this thread is value place(i) of the chunk: pieces of kVec
+  // Value i of this lane is value place(i) of the chunk: pieces of kVec
   // consecutive ones.  A row may start at any element, so the 16-byte loads
-  // are unaligned ones.
-  auto place = [&](int i) { return ((i / kVec) * kThreads + (int)threadIdx.x) * kVec + i % kVec; };
-  float v[kPerThread];
-  const int64_t left = V - base;  // values from the chunk's first to the row's end
+  // are unaligned ones.  They stay as loaded and are converted at each use.
+  auto place = [&](int i) { return ((i / kVec) * 64 + lane) * kVec + i % kVec; };
+  v4i raw[kIter];
+  if (V - base >= kChunk) {
 #pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    const int at = place(it * kVec);
-    T raw[kVec];
-    if (at + kVec <= left) {
-      __builtin_memcpy(raw, z + base + at, 16);
+    for (int it = 0; it < kIter; ++it) __builtin_memcpy(&raw[it], z + place(it * kVec), 16);
+  } else {
+    // the row's last chunk: -inf behind its end
+    const int left = (int)(V - base);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) v[it * kVec + e] = to_float(raw[e]);
-    } else {
+    for (int it = 0; it < kIter; ++it) {
+      const int at = place(it * kVec);
+      T t[kVec];
+      if (at + kVec <= left) {
+        __builtin_memcpy(t, z + at, 16);
+      } else {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) v[it * kVec + e] = at + e < left ? to_float(z[base + at + e]) : kNegInf;
+        for (int e = 0; e < kVec; ++e) t[e] = at + e < left ? z[at + e] : (T)kNegInf;
+      }
+      __builtin_memcpy(&raw[it], t, 16);
     }
   }
-  float gm[kGroups], mt = kNegInf;  // maxima of eight values each (a NaN is passed over), and of all
+  auto value = [&](int i) __attribute__((always_inline)) { return value_at(raw[i / kVec], i % kVec, (const T*)nullptr); };
+  float mt = value(0);  // a NaN stays one
 #pragma unroll
-  for (int a = 0; a < kGroups; ++a) {
-    gm[a] = v[8 * a];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) gm[a] = fmaxf(gm[a], v[8 * a + e]);
-    mt = fmaxf(mt, gm[a]);
-  }
-  tmax[threadIdx.x] = mt;
-  if (threadIdx.x == 0) ncand = 0;
-  if ((int)threadIdx.x < top) best[threadIdx.x] = 0;
-  __syncthreads();
-  float g = tmax[lane];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) g = fmaxf(g, tmax[lane + 64 * i]);
+  for (int i = 1; i < kPerLane; ++i) mt = __builtin_elementwise_maximum(mt, value(i));
   Stats st;
-  st.m = wave_max(g);
-  if (top > 0 && wave == 0) {
-    const float t = fmaxf(kth_of_wave(g, top), kLowest);  // -inf is never listed
-    if (lane == 0) lthr = t;
-  }
+  st.m = wave_max(mt);
   const float b = base_of(st.m);
   float S = 0.0f, W = 0.0f;  // W in powers of 2
+  if (fabsf(b) < kLargest) {
+    // (v - b) log2(e) as one fma: v L - c with c = fl(b L).  Every term is then
+    // 2^d too large for d = b L - c, which an fma gives exactly: taken out of
+    // the sums below.
+    const float c = b * kLog2E, d = __builtin_fmaf(b, kLog2E, -c);
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const float t = log2_term(v[i] - b);
-    const float e = __builtin_amdgcn_exp2f(t);
-    S += e;
-    W = __builtin_fmaf(e, t, W);
-  }
-  S = wave_sum(S);
-  W = wave_sum(W);
-  if (lane == 0) {
-    redS[wave] = S;
-    redW[wave] = W;
-  }
-  __syncthreads();
-  st.S = redS[0];
-  st.W = redW[0];
+    for (int i = 0; i < kPerLane; ++i) {
+      const float t = __builtin_elementwise_maximum(__builtin_fmaf(value(i), kLog2E, -c), kFloor);
+      const float e = __builtin_amdgcn_exp2f(t);
+      S += e;
+      W = __builtin_fmaf(e, t, W);
+    }
+    const float x = __builtin_amdgcn_exp2f(-d);
+    S *= x;
+    W = __builtin_fmaf(W, x, -d * S);
+  } else {  // b L may overflow (a NaN also comes here)
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) {
-    st.S += redS[i];
-    st.W += redW[i];
+    for (int i = 0; i < kPerLane; ++i) {
+      const float t = log2_term(value(i) - b);
+      const float e = __builtin_amdgcn_exp2f(t);
+      S += e;
+      W = __builtin_fmaf(e, t, W);
+    }
   }
+  st.S = wave_sum(S);
+  st.W = wave_sum(W);
 
   if (top > 0) {
-    const float t = lthr;
-    auto collect = [&](auto&& wanted) __attribute__((always_inline)) {
+    // All the chunk's values of at least t, `top` or more, are in these lanes:
+    // often `top` of them, whose values go through LDS to have one lane each.
+    const float t = fmaxf(kth_of_wave(mt, st.m, top), kLowest);  // -inf is never listed
+    const uint64_t lanes = __ballot(mt >= t);
+    if (lane < top) best[lane] = 0;
+    // f returns whether to go on.
+    auto visit = [&](auto&& f) __attribute__((always_inline)) {
+      for (uint64_t left = lanes; left != 0;) {
+        const int slot = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(left >> 32),
+                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)left, 0));
+        if ((left >> lane & 1) && slot < kHold) {
 #pragma unroll
-      for (int a = 0; a < kGroups; ++a) {
-        if (!wanted(gm[a])) continue;
-#pragma unroll
-        for (int i = 8 * a; i < 8 * a + 8; ++i) {
-          if (!wanted(v[i])) continue;
-          const int at = atomicAdd(&ncand, 1);
-          if (at < kCand) cand[at] = key_of(v[i], (uint32_t)(base + place(i)));
+          for (int it = 0; it < kIter; ++it) *reinterpret_cast<v4i*>(held + slot * kRow + it * 16) = raw[it];
         }
+        wave_sync();
+        for (int j = 0; j < kHold && left != 0; ++j, left &= left - 1) {
+          const int src = __builtin_ctzll(left);
+          const float v = to_float(reinterpret_cast<const T*>(held + j * kRow)[lane]);
+          if (!f(v, ((lane / kVec) * 64 + src) * kVec + lane % kVec)) return;
+        }
+        wave_sync();
       }
     };
-    collect([&](float x) { return x >= t; });
-    __syncthreads();
-    int n = ncand;
+    int n = 0;
+    auto collect = [&](bool in, float v, int at) __attribute__((always_inline)) {
+      const uint64_t who = __ballot(in);
+      const int to = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
+                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+      if (in && to < kCand) cand[to] = key_of(v, (uint32_t)(base + at));
+      n += __popcll(who);
+    };
+    visit([&](float v, int at) __attribute__((always_inline)) {
+      collect(v >= t, v, at);
+      return n <= kCand;
+    });
     if (n > kCand) {
       // Many values tie at t: rank the larger ones, mark the tied ones.
-      __syncthreads();
-      if (threadIdx.x == 0) ncand = 0;
-      for (int i = threadIdx.x; i < kChunk / 32; i += kThreads) tied[i] = 0;
-      __syncthreads();
-      collect([&](float x) { return x > t; });
-#pragma unroll
-      for (int it = 0; it < kIter; ++it) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) m |= v[it * kVec + e] == t ? 1u << e : 0u;
-        const int at = place(it * kVec);
-        if (m) atomicOr(&tied[at / 32], m << (at % 32));
-      }
-      __syncthreads();
-      n = ncand;
-      if (n <= kCand && n < top && wave == 0) {
+      for (int i = lane; i < kChunk / 32; i += 64) tied[i] = 0;
+      wave_sync();
+      n = 0;
+      visit([&](float v, int at) __attribute__((always_inline)) {
+        if (v == t) atomicOr(&tied[at / 32], 1u << (at % 32));
+        collect(v > t, v, at);
+        return n <= kCand;
+      });
+      if (n <= kCand && n < top) {
         // The first top - n marked values, in order: lane l has kPer words.
         constexpr int kPer = kChunk / 32 / 64;
         int mine = 0;
@@ -311,45 +348,47 @@ __global__ __launch_bounds__(kThreads) void logprobs_chunk_kernel(
       }
     }
     if (n <= kCand) {
-      rank_keys<kThreads>(cand, n, top, best);
+      wave_sync();
+      rank_keys<64>(cand, n, top, best);
     } else {
       // Many different values above t (a chunk whose large values share few
-      // groups): one maximum of the workgroup after the other.
+      // lanes): one maximum of the wave after the other.
       uint64_t last = ~0ull;
       for (int r = 0; r < top && last != 0; ++r) {
         uint64_t k = 0;
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-          const uint64_t c = v[i] > kNegInf ? key_of(v[i], (uint32_t)(base + place(i))) : 0;
+        visit([&](float v, int at) __attribute__((always_inline)) {
+          const uint64_t c = v >= t ? key_of(v, (uint32_t)(base + at)) : 0;
           if (c < last) k = max_u64(k, c);
-        }
-        last = block_max_key<kThreads>(k, redk);
-        if (threadIdx.x == 0) best[r] = last;
+          return true;
+        });
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) k = max_u64(k, shfl_xor_u64(k, off));
+        last = k;
+        if (lane == 0) best[r] = last;
       }
     }
-    __syncthreads();
+    wave_sync();
   }
   if (chunks == 1) {
-    write_row<T, kThreads>(z, V, row, st, best, tokens, ntok, top, lp, lse, ent, top_ids, top_lp);
+    write_row<T, 64>(z, V, row, st, best, tokens, ntok, top, lp, lse, ent, top_ids, top_lp);
     return;
   }
-  const int64_t slot = row * chunks + chunk;
-  if (threadIdx.x == 0) stats[slot] = st;
-  if ((int)threadIdx.x < top) keys[slot * top + threadIdx.x] = best[threadIdx.x];
+  if (lane == 0) stats[u] = st;
+  if (lane < top) keys[(int64_t)u * top + lane] = best[lane];
 }
 
 // Joins the chunks of one row.  Keys below a bound that at least `top` keys
 // reach are passed over: of fewer than `top` chunks, the least of the chunks'
-// q-th keys, q = ceil(top / chunks); of more, the top-th largest of 64 group
-// maxima of the chunks' first keys.
-template <typename T>
-__global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(
+// q-th keys, q = ceil(top / chunks); of more, one that `top` of 64 group maxima
+// of the chunks' first keys reach.
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void logprobs_join_kernel(
     const T* __restrict__ logits, int64_t ld, int64_t V, int chunks, int top, const Stats* __restrict__ stats,
     const uint64_t* __restrict__ keys, const int64_t* __restrict__ tokens, int64_t ntok, float* __restrict__ lp,
     float* __restrict__ lse, float* __restrict__ ent, int64_t* __restrict__ top_ids, float* __restrict__ top_lp) {
-  constexpr int kWaves = kJoinThreads / 64;
-  __shared__ float tmax[kJoinThreads];
-  __shared__ float heads[kJoinThreads];
+  constexpr int kWaves = NT / 64;
+  __shared__ float tmax[NT];
+  __shared__ float heads[NT];
   __shared__ float redS[kWaves], redW[kWaves];
   __shared__ uint64_t redk[kWaves];
   __shared__ uint64_t cand[kJoinCand];
@@ -368,13 +407,13 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(
   uint64_t k0[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t at = (int64_t)threadIdx.x + i * kJoinThreads;
+    const int64_t at = (int64_t)threadIdx.x + i * NT;
     k0[i] = at < n ? kr[at] : 0;
   }
-  for (int c = threadIdx.x; c < chunks; c += kJoinThreads) {
+  for (int c = threadIdx.x; c < chunks; c += NT) {
     const Stats s = sr[c];
     if (c == (int)threadIdx.x) s0 = s;
-    m = fmaxf(m, s.m);
+    m = __builtin_elementwise_maximum(m, s.m);
     if (top > 0) {
       const uint64_t k = kr[(int64_t)c * top + q - 1];
       const float h = k ? value_of(k) : kNegInf;
@@ -389,16 +428,16 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(
   float g = tmax[lane], h = heads[lane];
 #pragma unroll
   for (int i = 1; i < kWaves; ++i) {
-    g = fmaxf(g, tmax[lane + 64 * i]);
+    g = __builtin_elementwise_maximum(g, tmax[lane + 64 * i]);
     h = few ? fminf(h, heads[lane + 64 * i]) : fmaxf(h, heads[lane + 64 * i]);
   }
   Stats st;
   st.m = wave_max(g);
   float bound = kLowest;
-  if (top > 0) bound = fmaxf(few ? wave_min(h) : kth_of_wave(h, top), kLowest);
+  if (top > 0) bound = fmaxf(few ? wave_min(h) : kth_of_wave(h, wave_max(h), top), kLowest);
   const float b = base_of(st.m);
   float S = 0.0f, W = 0.0f;
-  for (int c = threadIdx.x; c < chunks; c += kJoinThreads) {
+  for (int c = threadIdx.x; c < chunks; c += NT) {
     const Stats s = c == (int)threadIdx.x ? s0 : sr[c];
     const float t = log2_term(s.m - b);  // sums of an empty chunk are 0
     const float e = __builtin_amdgcn_exp2f(t);
@@ -418,7 +457,7 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(
       if (at < kJoinCand) cand[at] = k0[i];
     }
   }
-  for (int64_t i = threadIdx.x + 4 * kJoinThreads; i < n; i += kJoinThreads) {
+  for (int64_t i = threadIdx.x + 4 * NT; i < n; i += NT) {
     const uint64_t k = kr[i];
     if (k != 0 && value_of(k) >= bound) {
       const int at = atomicAdd(&ncand, 1);
@@ -434,19 +473,19 @@ __global__ __launch_bounds__(kJoinThreads) void logprobs_join_kernel(
     st.W += redW[i];
   }
   if (ncand <= kJoinCand) {
-    rank_keys<kJoinThreads>(cand, ncand, top, best);
+    rank_keys<NT>(cand, ncand, top, best);
   } else {
     uint64_t last = ~0ull;
     for (int r = 0; r < top && last != 0; ++r) {
       uint64_t k = 0;
-      for (int64_t i = threadIdx.x; i < n; i += kJoinThreads)
+      for (int64_t i = threadIdx.x; i < n; i += NT)
         if (kr[i] < last) k = max_u64(k, kr[i]);
-      last = block_max_key<kJoinThreads>(k, redk);
+      last = block_max_key<NT>(k, redk);
       if (threadIdx.x == 0) best[r] = last;
     }
   }
   __syncthreads();
-  write_row<T, kJoinThreads>(logits + row * ld, V, row, st, best, tokens, ntok, top, lp, lse, ent, top_ids, top_lp);
+  write_row<T, NT>(logits + row * ld, V, row, st, best, tokens, ntok, top, lp, lse, ent, top_ids, top_lp);
 }
 
 template <typename T>
@@ -456,11 +495,22 @@ int launch(const void* logits, int64_t ld, const int64_t* tokens, int64_t ntok, 
   const T* z = static_cast<const T*>(logits);
   uint64_t* keys = static_cast<uint64_t*>(ws);  // 8-byte entries first
   Stats* stats = reinterpret_cast<Stats*>(keys + (chunks > 1 ? M * chunks * top : 0));
-  logprobs_chunk_kernel<T><<<(unsigned)(M * chunks), kThreads, 0, st>>>(z, ld, V, chunks, top, stats, keys, tokens, ntok,
-                                                                        lp, lse, ent, top_ids, top_lp);
-  if (chunks > 1)
-    logprobs_join_kernel<T><<<(unsigned)M, kJoinThreads, 0, st>>>(z, ld, V, chunks, top, stats, keys, tokens, ntok, lp,
-                                                                  lse, ent, top_ids, top_lp);
+  const unsigned total = (unsigned)(M * chunks);
+  // Few chunks: a wave per workgroup, to have them on as many CUs.
+  if (total <= 1024)
+    logprobs_chunk_kernel<T, 1><<<total, 64, 0, st>>>(z, ld, V, total, chunks, top, stats, keys, tokens, ntok, lp, lse,
+                                                      ent, top_ids, top_lp);
+  else
+    logprobs_chunk_kernel<T, 4><<<(total + 3) / 4, 256, 0, st>>>(z, ld, V, total, chunks, top, stats, keys, tokens, ntok,
+                                                                 lp, lse, ent, top_ids, top_lp);
+  // A wave per row while its lanes hold a few keys each (2048 rows of 104 keys:
+  // 10.5 us with four waves, 7).
+  if (chunks > 1 && chunks <= 64 && chunks * top <= 256)
+    logprobs_join_kernel<T, 64><<<(unsigned)M, 64, 0, st>>>(z, ld, V, chunks, top, stats, keys, tokens, ntok, lp, lse, ent,
+                                                            top_ids, top_lp);
+  else if (chunks > 1)
+    logprobs_join_kernel<T, 256><<<(unsigned)M, 256, 0, st>>>(z, ld, V, chunks, top, stats, keys, tokens, ntok, lp, lse,
+                                                              ent, top_ids, top_lp);
   return launch_status();
 }
 
@@ -472,7 +522,10 @@ int64_t token_logprobs_bytes(int64_t M, int64_t V, int top) {
   return chunks > 1 ? M * chunks * (8 * (int64_t)top + (int64_t)sizeof(Stats)) : 0;
 }
 
-int64_t token_logprobs_groups(int64_t M, int64_t V) { return M * ((V + kChunk - 1) / kChunk); }
+int64_t token_logprobs_groups(int64_t M, int64_t V) {
+  const int64_t chunks = (V + kChunk - 1) / kChunk;
+  return chunks > 1 ? (M * chunks + 3) / 4 > M ? (M * chunks + 3) / 4 : M : (M + 3) / 4;
+}
 
 int launch_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t ntok, int top,
                           float* lp, float* lse, float* ent, int64_t* top_ids, float* top_lp, void* ws, int64_t M,

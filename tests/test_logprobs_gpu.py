@@ -137,6 +137,17 @@ def test_large_values_and_peaked_rows():
     check(tensor(z, "f32"), rng.integers(0, v, (7, 4)), 10)
 
 
+@pytest.mark.parametrize("v", [9, 4096, 20000])
+def test_values_whose_multiples_overflow(v):
+    rng = np.random.default_rng(v + 11)
+    z = rng.uniform(2.0, 3.2, (4, v)) * 1e38
+    z[1] *= -1
+    z[2] = 1e30
+    z[3, 1:] = -3e38
+    z[3, 0] = -1e30
+    check(tensor(z, "f32"), rng.integers(0, v, (4, 3)), 6)
+
+
 @pytest.mark.parametrize("kind", list(TYPES))
 def test_strided_and_unaligned_rows(kind):
     rng = np.random.default_rng(5)
