@@ -7,7 +7,11 @@
 // All three read each value once with 16-byte loads, keep it in registers
 // between the absmax and the codes, and write each code once: they are bound
 // by HBM.  16 neighbouring lanes hold one 128-block, 8 values each, so the
-// absmax of a block is four cross-lane steps and no LDS.
+// absmax of a block is four cross-lane steps and no LDS.  Against a large
+// copy's rate: 8192 x 5120 bf16 24.9 us (floor 25), tiles of 17400 x 5120 bf16
+// 55 us (53), SwiGLU of 2048 x 17360 bf16 36.8 us (35); 16 x 5120 fp32 2.8 us
+// and SwiGLU of 4 x 9728 3.2 us are the latency of one load, one reduction and
+// one store.
 #include "fp8_math.h"
 
 namespace prism {
@@ -21,10 +25,16 @@ __device__ inline uint32_t max16(uint32_t m) {
   return m;
 }
 
-// h = g / (1 + exp(-g)) * u.  exp(-g) overflows to infinity for g < -88, where
-// the quotient is 0 as it should be.  __expf's error grows with |g| (about
-// |g| 2^-24 relative, 5e-6 at g = -80): four orders below a code's half step.
-__device__ inline float swiglu(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+// h = g / (1 + exp(-g)) * u as (g / 16) * (1 / (1 / 16 + exp(-g) / 16)) * u:
+// the reciprocal is v_rcp_f32 (1 ulp), and the 16 keeps it a normal number
+// down to g = -90; below it is 0.  exp's argument is one fma with the rounding
+// of fp32, |g| 2^-24 relative (5e-6 at g = -80).  All of it is four orders
+// below a code's half step, and an IEEE division would be a third of the
+// kernel's instructions (2048 x 17360 bf16: 42.3 us).
+__device__ inline float swiglu(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(g, -0x1.715476p+0f, -4.0f));
+  return g * 0x1p-4f * __builtin_amdgcn_rcpf(e + 0x1p-4f) * u;
+}
 
 // One 16-lane group per 1 x 128 block and step; a workgroup takes 16 rows by
 // U consecutive blocks.  GLU: x holds the gates, up the factors.
@@ -102,7 +112,16 @@ int launch_blocks(const void* x, const void* up, int64_t ld, uint8_t* q, float* 
   const int64_t rows16 = (M + 15) / 16;
   const T* xp = static_cast<const T*>(x);
   const T* upp = static_cast<const T*>(up);
-  quantize_blocks_kernel<T, 1, GLU><<<(unsigned)(rows16 * kb), 256, 0, st>>>(xp, upp, ld, q, scale, M, (int)K, kb);
+  // Two blocks a lane group once there are many workgroups per CU: fewer cache
+  // lines are shared by workgroups of different dies where rows do not start
+  // on a line (2048 x 17360 SwiGLU 38.8 -> 36.8 us; 8192 x 5120 26.4 -> 24.9;
+  // one block is faster below, 2048 x 2560 5.5 against 5.7).
+  if (rows16 * kb >= 4096) {
+    const int cg = (kb + 1) / 2;
+    quantize_blocks_kernel<T, 2, GLU><<<(unsigned)(rows16 * cg), 256, 0, st>>>(xp, upp, ld, q, scale, M, (int)K, cg);
+  } else {
+    quantize_blocks_kernel<T, 1, GLU><<<(unsigned)(rows16 * kb), 256, 0, st>>>(xp, upp, ld, q, scale, M, (int)K, kb);
+  }
   return launch_status();
 }
 

@@ -182,6 +182,21 @@ def test_swiglu(m, k, kind):
     assert ((got >= lo) & (got <= hi)).all()
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_rows_of_large_batches_quantize_as_in_small_ones(kind):
+    m, k = 1030, 8208  # over 4096 workgroups, an odd number of blocks, the last one partial
+    g = torch.Generator(device=DEV).manual_seed(12)
+    gu = (torch.randn((m, 2 * k), generator=g, device=DEV) * 3).to(TYPES[kind])
+    x, up = gu[:, :k], gu[:, k:]
+    q, s = prism.quantize_blocks_fp8(x)
+    h, hs = prism.swiglu_quantize_fp8(x, up)
+    for lo, hi in ((0, 16), (500, 501), (1010, 1030)):
+        q1, s1 = prism.quantize_blocks_fp8(x[lo:hi])
+        h1, hs1 = prism.swiglu_quantize_fp8(x[lo:hi], up[lo:hi])
+        assert torch.equal(q1.view(torch.uint8), q[lo:hi].view(torch.uint8)) and torch.equal(s1, s[:, lo:hi])
+        assert torch.equal(h1.view(torch.uint8), h[lo:hi].view(torch.uint8)) and torch.equal(hs1, hs[:, lo:hi])
+
+
 def test_swiglu_special_values():
     g = np.zeros((6, 128), np.float32)
     u = np.ones((6, 128), np.float32)
