@@ -125,25 +125,25 @@ __device__ inline v4f block_sum(const Operand16<true>& a, const Operand16<true>&
 
 // Few rows (M <= 16 MT): bound by reading the weights once.  A workgroup owns
 // 16 CB columns and its waves share out K: the chain over the blocks cannot be
-// split, but the blocks' sums can.  In rounds of WAVES x PER blocks, each wave
-// multiplies its PER blocks straight from global memory (a lane's operands are
+// split, but the blocks' sums can.  In rounds of WAVES blocks, each wave
+// multiplies its block straight from global memory (a lane's operands are
 // two 16-byte loads per row tile and block; those of the next round are
 // issued before this one's are used) and leaves the sums in LDS with the
 // blocks' scales s_a s_w; after one barrier, threads fold the round's blocks
 // into their outputs in order.  Rows past RP (4 where M <= 4) are not stored.
-template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES, int PER>
+template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_t* __restrict__ q,
                                                                     const float* __restrict__ s_a,
                                                                     const uint8_t* __restrict__ w,
                                                                     const float* __restrict__ s_w,
                                                                     OUT* __restrict__ y, int M, int N, int K) {
   static_assert(RP == 16 || (RP == 4 && MT == 1), "rows kept of a row tile");
-  constexpr int NT = 64 * WAVES, C = WAVES * PER;
+  constexpr int NT = 64 * WAVES;
   constexpr int kTile = 16 * RP;             // sums kept of a 16 x 16 tile
   constexpr int kOut = MT * CB * kTile;      // outputs of the workgroup
   constexpr int kPer = (kOut + NT - 1) / NT; // per thread
-  __shared__ __attribute__((aligned(16))) float lp[2][C][kOut];
-  __shared__ float ls[2][C][16 * MT];
+  __shared__ __attribute__((aligned(16))) float lp[2][WAVES][kOut];
+  __shared__ float ls[2][WAVES][16 * MT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r = lane & 15, g = lane >> 4;
   const int n0 = (int)blockIdx.x * 16 * CB;
@@ -153,47 +153,40 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_
   const float* swp = s_w + (size_t)(n0 / kBlock) * (size_t)KB;
 
   struct Round {
-    Frag16 x[PER][MT], w[PER][CB];
-    float sa[PER], sw[PER];  // lane l: the scales of row l (multiplied when used: here they would wait for all loads)
+    Frag16 x[MT], w[CB];
+    float sa, sw;  // lane l: the scales of row l (multiplied when used: here they would wait for all loads)
   };
   // Rows past M or N read zeros (past their buffer's end), as do chunks past K.
   auto load = [&](int b0, Round& d) __attribute__((always_inline)) {
+    const int b = b0 + wave;
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const int b = b0 + wave * PER + p;
+    for (int h = 0; h < 2; ++h) {
+      const int k = b * kBlock + 16 * g + 64 * h;
+      const bool in = k < K;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = b * kBlock + 16 * g + 64 * h;
-        const bool in = k < K;
+      for (int i = 0; i < MT; ++i)
+        d.x[i].c[h] = __builtin_amdgcn_raw_buffer_load_b128(
+            rx, in && 16 * i + r < M ? (uint32_t)((16 * i + r) * K + k) : kOutOfRange, 0, 0);
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-          d.x[p][i].c[h] = __builtin_amdgcn_raw_buffer_load_b128(
-              rx, in && 16 * i + r < M ? (uint32_t)((16 * i + r) * K + k) : kOutOfRange, 0, 0);
-#pragma unroll
-        for (int j = 0; j < CB; ++j)
-          d.w[p][j].c[h] = __builtin_amdgcn_raw_buffer_load_b128(
-              rw, in ? (uint32_t)((16 * j + r) * K + k) : kOutOfRange, 0, 0);
-      }
-      const int bb = b < KB ? b : KB - 1;  // blocks past K are not folded
-      d.sa[p] = s_a[(size_t)bb * (size_t)M + (lane < M ? lane : M - 1)];
-      d.sw[p] = swp[bb];
+      for (int j = 0; j < CB; ++j)
+        d.w[j].c[h] =
+            __builtin_amdgcn_raw_buffer_load_b128(rw, in ? (uint32_t)((16 * j + r) * K + k) : kOutOfRange, 0, 0);
     }
+    const int bb = b < KB ? b : KB - 1;  // blocks past K are not folded
+    d.sa = s_a[(size_t)bb * (size_t)M + (lane < M ? lane : M - 1)];
+    d.sw = swp[bb];
   };
   auto multiply = [&](int buf, const Round& d) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const int bl = wave * PER + p;
+    for (int i = 0; i < MT; ++i) {
+      const Operand16<EXACT> xo(d.x[i]);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const Operand16<EXACT> xo(d.x[p][i]);
-#pragma unroll
-        for (int j = 0; j < CB; ++j) {
-          const v4f v = block_sum(Operand16<EXACT>(d.w[p][j]), xo);
-          if (r < RP) *reinterpret_cast<v4f*>(&lp[buf][bl][(i * CB + j) * kTile + (g * RP + r) * 4]) = v;
-        }
+      for (int j = 0; j < CB; ++j) {
+        const v4f v = block_sum(Operand16<EXACT>(d.w[j]), xo);
+        if (r < RP) *reinterpret_cast<v4f*>(&lp[buf][wave][(i * CB + j) * kTile + (g * RP + r) * 4]) = v;
       }
-      if (lane < 16 * MT) ls[buf][bl][lane] = d.sa[p] * d.sw[p];
     }
+    if (lane < 16 * MT) ls[buf][wave][lane] = d.sa * d.sw;
   };
   float f[kPer];
 #pragma unroll
@@ -206,9 +199,9 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_
       const int m = 16 * (e / kTile / CB) + e / 4 % RP;
       const float* pv = &lp[buf][0][e];
       const float* sv = &ls[buf][0][m];
-      if (count == C) {
+      if (count == WAVES) {
 #pragma unroll 8
-        for (int b = 0; b < C; ++b) f[o] = __builtin_fmaf(pv[b * kOut], sv[b * 16 * MT], f[o]);
+        for (int b = 0; b < WAVES; ++b) f[o] = __builtin_fmaf(pv[b * kOut], sv[b * 16 * MT], f[o]);
       } else {
         for (int b = 0; b < count; ++b) f[o] = __builtin_fmaf(pv[b * kOut], sv[b * 16 * MT], f[o]);
       }
@@ -217,11 +210,11 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_
   Round cur, next;
   load(0, cur);
   int buf = 0;
-  for (int b0 = 0; b0 < KB; b0 += C) {
-    load(b0 + C, next);  // past K: zeros; behind a branch, the loads before it could not be awaited alone
+  for (int b0 = 0; b0 < KB; b0 += WAVES) {
+    load(b0 + WAVES, next);  // past K: zeros; behind a branch, the loads before it could not be awaited alone
     multiply(buf, cur);
     __syncthreads();  // also: every thread is done folding the round before last out of the other buffer
-    fold(buf, KB - b0 < C ? KB - b0 : C);
+    fold(buf, KB - b0 < WAVES ? KB - b0 : WAVES);
     cur = next;
     buf ^= 1;
   }
@@ -235,11 +228,11 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_
   }
 }
 
-template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES, int PER>
+template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES>
 void launch_small(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
                   hipStream_t st) {
-  gemm_fp8_small_kernel<OUT, EXACT, MT, RP, CB, WAVES, PER><<<(unsigned)((N + 16 * CB - 1) / (16 * CB)), 64 * WAVES, 0,
-                                                              st>>>(q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K);
+  gemm_fp8_small_kernel<OUT, EXACT, MT, RP, CB, WAVES><<<(unsigned)((N + 16 * CB - 1) / (16 * CB)), 64 * WAVES, 0, st>>>(
+      q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K);
 }
 
 // Waves and columns per workgroup by N: about 80 to 160 workgroups of eight
@@ -250,9 +243,9 @@ template <typename OUT, bool EXACT>
 void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N,
                        int K, hipStream_t st) {
 #define PRISM_FP8_SMALL(MT, RP)                                                                    \
-  if (N <= 3840) launch_small<OUT, EXACT, MT, RP, 1, 8, 1>(q, s_a, w, s_w, y, M, N, K, st);         \
-  else if (N <= 8192) launch_small<OUT, EXACT, MT, RP, 2, 8, 1>(q, s_a, w, s_w, y, M, N, K, st);    \
-  else launch_small<OUT, EXACT, MT, RP, 1, 4, 1>(q, s_a, w, s_w, y, M, N, K, st)
+  if (N <= 3840) launch_small<OUT, EXACT, MT, RP, 1, 8>(q, s_a, w, s_w, y, M, N, K, st);         \
+  else if (N <= 8192) launch_small<OUT, EXACT, MT, RP, 2, 8>(q, s_a, w, s_w, y, M, N, K, st);    \
+  else launch_small<OUT, EXACT, MT, RP, 1, 4>(q, s_a, w, s_w, y, M, N, K, st)
   if (M <= 4) {
     PRISM_FP8_SMALL(1, 4);
   } else if (M <= 16) {

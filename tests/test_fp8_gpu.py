@@ -315,6 +315,21 @@ def test_gemm_rows_do_not_depend_on_the_batch(n, k, kind):
     assert torch.equal(run(pick), big)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,n,k", [(260, 17800, 272), (1000, 9728, 400), (4096, 4096, 144), (700, 9728, 1168),
+                                   (2300, 9728, 272), (5000, 640, 656), (1100, 1300, 2064), (1500, 5120, 272),
+                                   (8192, 1300, 400)])
+def test_gemm_outputs_are_those_of_small_batches(m, n, k, kind):
+    """Every output of every tile size, with whole, partial and cut last rounds, against calls of 60 rows or fewer."""
+    g = torch.Generator(device=DEV).manual_seed(m + n + k)
+    q, sa = prism.quantize_blocks_fp8(torch.randn((m, k), generator=g, device=DEV))
+    w, sw = prism.quantize_tiles_fp8(torch.randn((n, k), generator=g, device=DEV))
+    y = bits(prism.gemm_fp8_blockscale(q, sa, w, sw, out_dtype=TYPES[kind]))
+    for lo in range(0, m, 60):
+        part = prism.gemm_fp8_blockscale(q[lo:lo + 60], sa[:, lo:lo + 60].contiguous(), w, sw, out_dtype=TYPES[kind])
+        assert torch.equal(bits(part), y[lo:lo + 60]), lo
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_gemm_special_values(kind):
     """A NaN scale (a block with a NaN or infinity) spoils its own row only; a NaN code its row or column; zero
