@@ -39,6 +39,21 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 // Workgroup barrier that the compiler may not move memory accesses across.
 __device__ inline void barrier() { asm volatile("s_barrier" ::: "memory"); }
 
+// Orders a wave's own LDS accesses, which the hardware keeps in order.
+__device__ inline void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// f rounded to an output.  f is opaque here: the compiler would otherwise make
+// one instruction of the last fma and the rounding to fp16, without the fp32
+// rounding between them, in some kernels and not in others.
+template <typename OUT>
+__device__ inline OUT rounded(float f) {
+  asm("" : "+v"(f));
+  return (OUT)f;
+}
+
 // s_waitcnt lgkmcnt(0), no wait on vmcnt or expcnt (gfx9 encoding).
 __device__ inline void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
 
@@ -224,7 +239,7 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_
     if (e >= kOut) break;
     const int t = e / kTile, m = 16 * (t / CB) + e / 4 % RP;
     const int n = n0 + 16 * (t % CB) + 4 * (e % kTile / (4 * RP)) + e % 4;
-    if (m < M && n < N) y[(size_t)m * (size_t)N + (size_t)n] = (OUT)f[o];
+    if (m < M && n < N) y[(size_t)m * (size_t)N + (size_t)n] = rounded<OUT>(f[o]);
   }
 }
 
@@ -258,12 +273,6 @@ void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, con
 #undef PRISM_FP8_SMALL
 }
 
-// Four consecutive outputs of a row, rounded once each.
-template <typename OUT>
-struct alignas(4 * sizeof(OUT)) Out4 {
-  OUT v[4];
-};
-
 // LDS-tiled kernel.  One workgroup of 2 x WN waves owns BM = 32 TM rows by BN =
 // 16 TN WN columns and walks K one 128-block (a stage) at a time; a stage is
 // the block's BM + BN rows of 128 codes and the rows' scales, copied directly
@@ -271,7 +280,7 @@ struct alignas(4 * sizeof(OUT)) Out4 {
 //
 // A lane holds four consecutive columns of one row of each 16 x 16 tile: its
 // row scale is one value per 16 rows, the fold one multiplication per 16 rows
-// and one fma per output, and y is written in pieces of four.  Frag row p of
+// and one fma per output, and y leaves as whole rows.  Frag row p of
 // column tile j is weight row 4 TN (p / 4) + 4 j + p % 4 of the wave's 16 TN,
 // which makes a lane's columns over its tiles consecutive.
 //
@@ -520,31 +529,48 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   }
 #pragma unroll
   for (int t = 0; t < kLag; ++t) fold(tile(kT - kLag + t), col(kT - kLag + t), p[t], scp[(kT - kLag + t) % 2]);
-  tiled::dma::wait_vmcnt<0>();  // no copy may land in LDS after the workgroup ends
+  tiled::dma::wait_vmcnt<0>();
+  __syncthreads();  // every copy has landed and every wave has read its last: the buffers are free
 
-  // A lane's 16 columns n .. n + 15 of each of its rows.
-  const int n = n0 + wn * 16 * TN + 4 * TN * g;
-  const bool wide = N % 4 == 0 && reinterpret_cast<uintptr_t>(y) % sizeof(Out4<OUT>) == 0;
+  // A lane holds 4 TN consecutive columns of one of 16 rows.  Through LDS (its
+  // wave's own part) those rows are stored whole, 16 bytes a lane: a lane's own
+  // pieces would leave gaps between the lanes' (us, stored directly and so:
+  // fp32 8192 x 5120 x 5120 403 and 381, bf16 202 and 195, 5585 x 3667 x 160 39
+  // and 23, bf16 27 and 18).  Rows of y start anywhere where N is odd, so these
+  // are unaligned stores (element by element the last took 78 us).
+  constexpr int kVec = 16 / (int)sizeof(OUT);
+  constexpr int kChunks = 16 * TN / kVec;    // of a row
+  constexpr int kPitch = 16 * kChunks + 16;  // 16 more bytes against bank conflicts
+  static_assert(2 * WN * 16 * kPitch <= kTileLds<WN, TM, TN, R>, "LDS of the outputs");
+  int8_t* const part = lds + wave * 16 * kPitch;
+  const int n = n0 + wn * 16 * TN + lane % kChunks * kVec;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = m0 + xrow + 16 * i;
-    if (m >= M) continue;
-    OUT* yr = y + (size_t)m * (size_t)N;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      if (wide) {
-        if (n + 4 * j < N) {
-          Out4<OUT> o;
+    for (int c = 0; c < 4 * TN; c += kVec) {
+      OUT o[kVec];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o.v[e] = (OUT)f[TN * i + j][e];
-          *reinterpret_cast<Out4<OUT>*>(yr + n + 4 * j) = o;
-        }
+      for (int e = 0; e < kVec; ++e) o[e] = rounded<OUT>(f[TN * i + (c + e) / 4][e % 4]);
+      __builtin_memcpy(__builtin_assume_aligned(part + r * kPitch + (4 * TN * g + c) * (int)sizeof(OUT), 16), o, 16);
+    }
+    wave_order();
+#pragma unroll
+    for (int t = 0; t < kChunks / 4; ++t) {
+      const int row = lane / kChunks + t * (64 / kChunks);
+      const int m = m0 + (wm * TM + i) * 16 + row;
+      OUT o[kVec];
+      __builtin_memcpy(o, __builtin_assume_aligned(part + row * kPitch + lane % kChunks * 16, 16), 16);
+      if (m >= M) continue;
+      OUT* yr = y + (size_t)m * (size_t)N;
+      if (n + kVec <= N) {
+        __builtin_memcpy(yr + n, o, 16);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + 4 * j + e < N) yr[n + 4 * j + e] = (OUT)f[TN * i + j][e];
+        for (int e = 0; e < kVec; ++e)
+          if (n + e < N) yr[n + e] = o[e];
       }
     }
+    wave_order();
   }
 }
 
