@@ -626,17 +626,18 @@ constexpr int kCus = 256;
 //    16: 64 x 64 tiles 20.6 against 24.0), up to 32 rows where N <= 6144 (5120
 //    x 5120, M = 32: 11.9 against 15.0), for an fp32 y up to 64 rows there
 //    (5120 x 5120, M = 64: 18.5 against 22.5);
-//  * 64 x 64 tiles while they fit the CUs at once (128 x 5120 x 5120: 15.3,
-//    64 x 128 tiles 18.1), for an fp32 y, which is bound by the MFMAs and
-//    conversions of a wave, up to five per CU (512 x 9728 x 2560: 38 against 43
-//    with 128 x 128; 2048 x 5120 x 5120 the other way, 119 against 142);
-//  * 16-bit y: 64 x 128 tiles while they fit the CUs at once (500 x 2560 x
-//    9680: 34.9, 64 x 64 40.6, 128 x 128 47);
-//  * else the smallest estimate of 128 x 128, 192 x 256 and 256 x 256 tiles:
-//    rounds of the CUs (two workgroups each for 128 x 128) times a round's
-//    cost relative to 256 x 256; 256 x 256 tiles that fill at most half of
-//    their last round are cut in two there, for 0.6 of a round (8192 x 5120 x
-//    5120: 221 -> 200).
+//  * 16-bit y: 64 x 64 tiles while they fit the CUs at once (128 x 5120 x 5120:
+//    15.1, 64 x 128 tiles 18.2), 64 x 128 tiles while those do (500 x 2560 x
+//    9680: 34.9, 64 x 64 40.6, 128 x 128 47), else the smallest estimate of
+//    128 x 128, 192 x 256 and 256 x 256 tiles (K = 5120: 768 x 5120 32.8, 58.3
+//    and 44.2; 2048 x 5120 73.6, 61.2 and 65.2; 1536 x 9728 94, 110 and 71);
+//  * fp32 y, bound by the MFMAs and conversions of a wave: the smaller estimate
+//    of 64 x 64 and 128 x 128 tiles (K = 5120: 1024 x 2560 42.6 and 49.7; 768 x
+//    5120 58.7 and 51.6; 2048 x 5120 135 and 116).
+// An estimate counts rounds of the CUs, relative to a full round of 256 x 256
+// tiles, or with an fp32 y of two 128 x 128 tiles per CU.  One workgroup per CU
+// of the latter takes two thirds of the time of two; 256 x 256 tiles that fill
+// at most half of their last round are cut in two there, for 0.6 of a round.
 template <typename OUT, bool EXACT>
 int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
            hipStream_t st) {
@@ -645,18 +646,23 @@ int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_
   launch_tile<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC>(q, s_a, w, s_w, y, M, N, K, (int)(FULL), st)
   if (M <= 8 || (M <= 16 && N <= 16384) || (M <= (EXACT ? 64 : 32) && N <= 6144)) {
     launch_small_rows<OUT, EXACT>(q, s_a, w, s_w, y, M, N, K, st);
-  } else if (tiles(64, 64) <= (EXACT ? 5 : 1) * kCus) {
-    PRISM_FP8_TILE(2, 2, 2, 3, 2, 3, 3, tiles(64, 64));
-  } else if constexpr (EXACT) {
-    PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, tiles(128, 128));
+    return launch_status();
+  }
+  const int64_t t64 = tiles(64, 64), t128 = tiles(128, 128), rest = t128 % (2 * kCus);
+  const float c128 = (float)(t128 / (2 * kCus)) + (rest == 0 ? 0.0f : rest <= kCus ? 0.66f : 1.0f);
+  if constexpr (EXACT) {
+    const float c64 = 0.12f + 0.165f * (float)((t64 + kCus - 1) / kCus);
+    if (c64 < c128) PRISM_FP8_TILE(2, 2, 2, 3, 2, 3, 3, t64);
+    else PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, t128);
+  } else if (t64 <= kCus) {
+    PRISM_FP8_TILE(2, 2, 2, 3, 2, 3, 3, t64);
   } else if (tiles(64, 128) <= kCus) {
     PRISM_FP8_TILE(4, 2, 2, 3, 2, 3, 2, tiles(64, 128));
   } else {
     const int64_t t256 = tiles(256, 256), last = t256 % kCus;
     const float c256 = (float)(t256 / kCus) + (last == 0 ? 0.0f : 2 * last <= kCus ? 0.6f : 1.0f);
-    const float c192 = 0.8f * (float)((tiles(192, 256) + kCus - 1) / kCus);
-    const float c128 = 0.64f * (float)((tiles(128, 128) + 2 * kCus - 1) / (2 * kCus));
-    if (c128 < c192 && c128 < c256) PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, tiles(128, 128));
+    const float c192 = 0.83f * (float)((tiles(192, 256) + kCus - 1) / kCus);
+    if (0.68f * c128 < c192 && 0.68f * c128 < c256) PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, t128);
     else if (c192 < c256) PRISM_FP8_TILE(4, 6, 4, 2, 6, 2, 1, tiles(192, 256));
     else PRISM_FP8_TILE(4, 8, 4, 2, 4, 2, 1, 2 * last <= kCus ? t256 - last : t256);
   }
