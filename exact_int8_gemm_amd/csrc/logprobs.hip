@@ -13,18 +13,21 @@
 // wave each, so a row's sums are always added in the same order.  A chunk is
 // read once and stays in registers: maximum, sums, and its `top` largest
 // values; a second kernel joins the chunks of a row.  Waves do not wait for
-// each other and stay small: 56 registers, for 8 waves a SIMD.  2048 x 100003
-// bf16, top 8: 98 to 108 us (410 MB: 81 us at a large copy's rate) and 7 us for
-// the join.  With four waves and five barriers to each 8192 values, which left
-// the vector units idle 40% of the time, it took 143 us.  What bounds it now is
-// issue: per value an exp at a quarter of the rate and six other instructions.
+// each other.  2048 x 100003 bf16, both kernels: 95 us with top 8, 73 without
+// (410 MB: 81 us at a large copy's rate).  With four waves and five barriers to
+// each 8192 values, which left the vector units idle 40% of the time, it took
+// 150 us.  What bounds it now is issue: per value an exp at a quarter of the
+// rate and six other instructions; held to 96 or fewer registers for more
+// waves, the kernel spills (105 us).
 //
 // Top values: a bisection finds a value t that at least `top` of the 64 lanes'
-// maxima reach, and often no more.  The values of those lanes alone are looked
-// at (of all lanes: 144 us instead of 108); the ones of at least t (a few more than `top`) are ranked, by value and
-// then by index, as one 64-bit key each.  When too many values tie at t (a
-// chunk masked to one finite value), the larger ones are ranked and the tied
-// ones marked in a bit per value, of which the first are taken.
+// maxima reach, and often no more.  Only the 16-byte pieces with values of at
+// least t are looked at, through LDS (95 us; all values of the lanes that have
+// such, 102; of all lanes, 144); those values, a few more than `top`, are
+// ranked by value and then by index, as one 64-bit key each.  When too many
+// values tie at t (a chunk masked to one finite value), the larger ones are
+// ranked and the tied ones marked in a bit per value, of which the first are
+// taken.
 #include "../../include/prism.h"
 #include "prism_internal.h"
 
@@ -34,7 +37,8 @@ namespace {
 constexpr int kPerLane = 64;
 constexpr int kChunk = 64 * kPerLane;
 constexpr int kCand = 128;  // candidates of a chunk ranked at once
-constexpr int kHold = 16;   // lanes whose values are held in LDS at once
+constexpr int kPieces = 64; // 16-byte pieces with candidates that are held in LDS
+constexpr int kHold = 16;   // lanes whose values are held there at once
 constexpr int kJoinCand = 1024;
 constexpr float kLowest = -3.402823466e+38f;
 constexpr float kLog2E = 0x1.715476p+0f, kLn2 = 0x1.62e430p-1f;
@@ -136,6 +140,11 @@ __device__ inline float kth_of_wave(float g, float largest, int top) {
   return of_order(__builtin_amdgcn_readfirstlane(lo));
 }
 
+// Lanes below this one in a mask.
+__device__ inline int lanes_below(uint64_t mask) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
 // Orders this wave's LDS accesses: what its lanes wrote before is read after.
 __device__ inline void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -211,6 +220,8 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
   constexpr int kIter = kPerLane / kVec;
   constexpr int kRow = kPerLane * (int)sizeof(T) + 16;  // 16 more bytes against bank conflicts
   __shared__ __attribute__((aligned(16))) uint8_t lheld[WAVES][kHold * kRow];
+  static_assert(kHold * kRow >= kPieces * 16, "pieces share the lanes' LDS");
+  __shared__ uint16_t lplaces[WAVES][kPieces];
   __shared__ uint64_t lcand[WAVES][kCand];
   __shared__ uint64_t lbest[WAVES][PRISM_TOP_MAX];
   __shared__ uint32_t ltied[WAVES][kChunk / 32];
@@ -218,6 +229,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
   const unsigned u = blockIdx.x * WAVES + (unsigned)wave;
   if (u >= total) return;  // no barrier below
   uint8_t* held = lheld[wave];
+  uint16_t* places = lplaces[wave];
   uint64_t* cand = lcand[wave];
   uint64_t* best = lbest[wave];
   uint32_t* tied = ltied[wave];
@@ -250,9 +262,14 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
     }
   }
   auto value = [&](int i) __attribute__((always_inline)) { return value_at(raw[i / kVec], i % kVec, (const T*)nullptr); };
-  float mt = value(0);  // a NaN stays one
+  float gm[kIter], mt = kNegInf;  // maxima of the pieces, and of all; a NaN stays one
 #pragma unroll
-  for (int i = 1; i < kPerLane; ++i) mt = __builtin_elementwise_maximum(mt, value(i));
+  for (int it = 0; it < kIter; ++it) {
+    gm[it] = value(it * kVec);
+#pragma unroll
+    for (int e = 1; e < kVec; ++e) gm[it] = __builtin_elementwise_maximum(gm[it], value(it * kVec + e));
+    mt = __builtin_elementwise_maximum(mt, gm[it]);
+  }
   Stats st;
   st.m = wave_max(mt);
   const float b = base_of(st.m);
@@ -285,16 +302,37 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
   st.W = wave_sum(W);
 
   if (top > 0) {
-    // All the chunk's values of at least t, `top` or more, are in these lanes:
-    // often `top` of them, whose values go through LDS to have one lane each.
     const float t = fmaxf(kth_of_wave(mt, st.m, top), kLowest);  // -inf is never listed
-    const uint64_t lanes = __ballot(mt >= t);
     if (lane < top) best[lane] = 0;
-    // f returns whether to go on.
+    int n = 0;
+    auto collect = [&](bool in, float v, int at) __attribute__((always_inline)) {
+      const uint64_t who = __ballot(in);
+      const int to = n + lanes_below(who);
+      if (in && to < kCand) cand[to] = key_of(v, (uint32_t)(base + at));
+      n += __popcll(who);
+    };
+    // The pieces with values of at least t, a few more than `top`, go to LDS,
+    // to have a lane for each of their values.
+    int np = 0;
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const bool in = gm[it] >= t;
+      const uint64_t who = __ballot(in);
+      if (!who) continue;
+      const int to = np + lanes_below(who);
+      if (in && to < kPieces) {
+        *reinterpret_cast<v4i*>(held + to * 16) = raw[it];
+        places[to] = (uint16_t)place(it * kVec);
+      }
+      np += __popcll(who);
+    }
+    wave_sync();
+    // Where they do not fit, the lanes with values of at least t are looked at
+    // whole, one after the other; f returns whether to go on.
+    const uint64_t lanes = __ballot(mt >= t);
     auto visit = [&](auto&& f) __attribute__((always_inline)) {
       for (uint64_t left = lanes; left != 0;) {
-        const int slot = (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(left >> 32),
-                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)left, 0));
+        const int slot = lanes_below(left);
         if ((left >> lane & 1) && slot < kHold) {
 #pragma unroll
           for (int it = 0; it < kIter; ++it) *reinterpret_cast<v4i*>(held + slot * kRow + it * 16) = raw[it];
@@ -308,18 +346,17 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
         wave_sync();
       }
     };
-    int n = 0;
-    auto collect = [&](bool in, float v, int at) __attribute__((always_inline)) {
-      const uint64_t who = __ballot(in);
-      const int to = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32),
-                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-      if (in && to < kCand) cand[to] = key_of(v, (uint32_t)(base + at));
-      n += __popcll(who);
-    };
-    visit([&](float v, int at) __attribute__((always_inline)) {
-      collect(v >= t, v, at);
-      return n <= kCand;
-    });
+    if (np <= kPieces) {
+      for (int i = lane; i - lane < np * kVec; i += 64) {
+        const float v = to_float(reinterpret_cast<const T*>(held)[i]);  // of 64 kVec: past np stale ones
+        collect(i < np * kVec && v >= t, v, places[i / kVec] + i % kVec);
+      }
+    } else {
+      visit([&](float v, int at) __attribute__((always_inline)) {
+        collect(v >= t, v, at);
+        return n <= kCand;
+      });
+    }
     if (n > kCand) {
       // Many values tie at t: rank the larger ones, mark the tied ones.
       for (int i = lane; i < kChunk / 32; i += 64) tied[i] = 0;
