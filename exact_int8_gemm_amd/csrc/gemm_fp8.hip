@@ -146,6 +146,9 @@ __device__ inline v4f block_sum(const Operand16<true>& a, const Operand16<true>&
 // issued before this one's are used) and leaves the sums in LDS with the
 // blocks' scales s_a s_w; after one barrier, threads fold the round's blocks
 // into their outputs in order.  Rows past RP (4 where M <= 4) are not stored.
+// M = 1, 5120 x 5120, bf16: 7.3 us with weights in the cache behind the L2s, 8.9
+// from HBM (26 MB: 5.2 at a large copy's rate, which 100003 x 2560 at M = 4
+// reaches: 46 to 49 us, 5.4 TB/s).
 template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_t* __restrict__ q,
                                                                     const float* __restrict__ s_a,
@@ -257,19 +260,23 @@ void launch_small(const uint8_t* q, const float* s_a, const uint8_t* w, const fl
 template <typename OUT, bool EXACT>
 void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N,
                        int K, hipStream_t st) {
-#define PRISM_FP8_SMALL(MT, RP)                                                                    \
-  if (N <= 3840) launch_small<OUT, EXACT, MT, RP, 1, 8>(q, s_a, w, s_w, y, M, N, K, st);         \
-  else if (N <= 8192) launch_small<OUT, EXACT, MT, RP, 2, 8>(q, s_a, w, s_w, y, M, N, K, st);    \
-  else launch_small<OUT, EXACT, MT, RP, 1, 4>(q, s_a, w, s_w, y, M, N, K, st)
+#define PRISM_FP8_SMALL(MT, RP, CB, WAVES) launch_small<OUT, EXACT, MT, RP, CB, WAVES>(q, s_a, w, s_w, y, M, N, K, st)
+#define PRISM_FP8_SMALL_N(MT, RP)                     \
+  if (N <= 3840) PRISM_FP8_SMALL(MT, RP, 1, 8);       \
+  else if (N <= 8192) PRISM_FP8_SMALL(MT, RP, 2, 8);  \
+  else PRISM_FP8_SMALL(MT, RP, 1, 4)
   if (M <= 4) {
-    PRISM_FP8_SMALL(1, 4);
+    PRISM_FP8_SMALL_N(1, 4);
   } else if (M <= 16) {
-    PRISM_FP8_SMALL(1, 16);
-  } else if (M <= 32) {
-    PRISM_FP8_SMALL(2, 16);
+    PRISM_FP8_SMALL_N(1, 16);
+  } else if (M <= 32) {  // N <= 6144 from here on
+    if (N <= 3840) PRISM_FP8_SMALL(2, 16, 1, 8);
+    else PRISM_FP8_SMALL(2, 16, 2, 8);
   } else if constexpr (EXACT) {
-    PRISM_FP8_SMALL(4, 16);
+    if (N <= 3840) PRISM_FP8_SMALL(4, 16, 1, 8);
+    else PRISM_FP8_SMALL(4, 16, 2, 8);
   }
+#undef PRISM_FP8_SMALL_N
 #undef PRISM_FP8_SMALL
 }
 
@@ -300,7 +307,7 @@ void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, con
 // taken away, the kernels take the same time).
 //
 // What bounds the 256 x 256 form, MI355X, M = N = K = 8192 (480-510 us, 2.2
-// PFLOP/s; 8192 x 5120 x 5120: 200 us, 2.1 PFLOP/s): the matrix cores are busy
+// PFLOP/s; 8192 x 5120 x 5120: 195 us, 2.2 PFLOP/s): the matrix cores are busy
 // 58% of the cycles at a clock that the power limit holds at 1.9 GHz; without
 // the copies it takes 423 us, without the LDS reads 416, without the folds
 // 405, without either barrier 465.  Times of these parts add up rather than
@@ -308,6 +315,13 @@ void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, con
 // not kept: 32 x 32 x 64 MFMAs (4% slower at 8192), all copies of a stage
 // issued together (265 against 225 us at 8192 x 5120 x 5120), one barrier per
 // stage (4% slower), 128 x 128 tiles of four waves (twice the copies: 560 us).
+//
+// The smaller forms are bound by their copies, 20 to 33 bytes a clock and CU
+// whatever R is (500 x 2560 x 9680, 160 tiles of 64 x 128: 34 us with inputs in
+// the cache behind the L2s, 47 from HBM, where rows that start inside a cache
+// line cost two requests a copy: 31 at K = 9600).  The fp32 form, 128 x 128, is
+// bound by the f16 MFMAs and the conversions (8192 x 5120 x 5120: 381 us, 53%
+// busy; 305 at the rate of a large 16-bit library product).
 template <int WN, int TM, int TN, int R>
 constexpr int kTileLds = R * ((32 * TM + 16 * TN * WN) * kBlock + 128 * WN * 4);  // R stages
 
