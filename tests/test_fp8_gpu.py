@@ -402,6 +402,28 @@ def test_gemm_outputs_past_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gemm_weights_past_32_bit_offsets(kind):
+    """Weights of over 2^32 bytes at the largest K: the last columns are those of a call with the last weight rows."""
+    n, k = 33000, 131040
+    assert n * k > 2 ** 32
+    cut = n // 128 * 128 - 256
+    kb, nb = -(-k // 128), -(-n // 128)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    w = torch.zeros((n, k), dtype=torch.uint8, device=DEV)
+    w[cut:] = torch.randint(0, 120, (n - cut, k), generator=g, device=DEV).to(torch.uint8)
+    w = w.view(prism.FP8)
+    sw = torch.rand((nb, kb), generator=g, device=DEV)
+    for m in (2, 70):
+        q, sa = prism.quantize_blocks_fp8(torch.randn((m, k), generator=g, device=DEV))
+        y = prism.gemm_fp8_blockscale(q, sa, w, sw, out_dtype=TYPES[kind])
+        part = prism.gemm_fp8_blockscale(q, sa, w[cut:].contiguous(), sw[cut // 128:].contiguous(), out_dtype=TYPES[kind])
+        assert torch.equal(bits(y[:, cut:].contiguous()), bits(part)) and (y[:, :cut] == 0).all()
+        assert (part != 0).any()
+    del w, y
+    torch.cuda.empty_cache()
+
+
 def test_quantize_inputs_past_32_bit_offsets():
     ld, m = 1 << 20, 2100
     buf = torch.zeros((m * ld,), dtype=torch.bfloat16, device=DEV)
