@@ -26,8 +26,9 @@
 // such, 102; of all lanes, 144); those values, a few more than `top`, are
 // ranked by value and then by index, as one 64-bit key each.  When too many
 // values tie at t (a chunk masked to one finite value), the larger ones are
-// ranked and the tied ones marked in a bit per value, of which the first are
-// taken.
+// ranked and the tied ones marked, of which the first are taken; the join then
+// merges the chunks' sorted keys (256 x 100003 f16, all of the lowest value, top
+// 20: 20 and 8 us; 51 MB).
 #include "../../include/prism.h"
 #include "prism_internal.h"
 
@@ -40,6 +41,7 @@ constexpr int kCand = 128;  // candidates of a chunk ranked at once
 constexpr int kPieces = 64; // 16-byte pieces with candidates that are held in LDS
 constexpr int kHold = 16;   // lanes whose values are held there at once
 constexpr int kJoinCand = 1024;
+constexpr int kRankCand = 128;  // of the keys of up to 64 chunks: more are merged
 constexpr float kLowest = -3.402823466e+38f;
 constexpr float kLog2E = 0x1.715476p+0f, kLn2 = 0x1.62e430p-1f;
 constexpr float kNegInf = -__builtin_inff();
@@ -103,6 +105,24 @@ template <int CTRL, int ROWS>
 __device__ inline float dpp(float v, float old) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, old), __builtin_bit_cast(int, v),
                                                                CTRL, ROWS, 0xf, false));
+}
+template <int CTRL, int ROWS>
+__device__ inline uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false));
+}
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = dpp_max<0x111, 0xf>(v);  // the steps of wave_reduce below
+  v = dpp_max<0x112, 0xf>(v);
+  v = dpp_max<0x114, 0xf>(v);
+  v = dpp_max<0x118, 0xf>(v);
+  v = dpp_max<0x142, 0xa>(v);
+  v = dpp_max<0x143, 0xc>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ inline uint64_t wave_max_key(uint64_t k) {
+  const uint32_t hi = wave_max((uint32_t)(k >> 32));
+  const uint32_t lo = wave_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return ((uint64_t)hi << 32) | lo;
 }
 template <typename F>
 __device__ inline float wave_reduce(float v, float neutral, F op) {
@@ -224,7 +244,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
   __shared__ uint16_t lplaces[WAVES][kPieces];
   __shared__ uint64_t lcand[WAVES][kCand];
   __shared__ uint64_t lbest[WAVES][PRISM_TOP_MAX];
-  __shared__ uint32_t ltied[WAVES][kChunk / 32];
+  __shared__ uint8_t ltied[WAVES][64 * kIter];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const unsigned u = blockIdx.x * WAVES + (unsigned)wave;
   if (u >= total) return;  // no barrier below
@@ -232,7 +252,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
   uint16_t* places = lplaces[wave];
   uint64_t* cand = lcand[wave];
   uint64_t* best = lbest[wave];
-  uint32_t* tied = ltied[wave];
+  uint8_t* tied = ltied[wave];
   const int64_t row = u / (unsigned)chunks;
   const int64_t base = (int64_t)(u % (unsigned)chunks) * kChunk;
   const T* z = logits + row * ld + base;
@@ -311,27 +331,37 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
       if (in && to < kCand) cand[to] = key_of(v, (uint32_t)(base + at));
       n += __popcll(who);
     };
-    // The pieces with values of at least t, a few more than `top`, go to LDS,
-    // to have a lane for each of their values.
-    int np = 0;
+    // Pieces whose maximum is wanted go to LDS, to have a lane for each of their
+    // values; where there are more than kPieces of them, only their number counts.
+    auto gather = [&](auto&& wanted) __attribute__((always_inline)) {
+      int np = 0;
+      wave_sync();
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const bool in = gm[it] >= t;
-      const uint64_t who = __ballot(in);
-      if (!who) continue;
-      const int to = np + lanes_below(who);
-      if (in && to < kPieces) {
-        *reinterpret_cast<v4i*>(held + to * 16) = raw[it];
-        places[to] = (uint16_t)place(it * kVec);
+      for (int it = 0; it < kIter; ++it) {
+        const bool in = wanted(gm[it]);
+        const uint64_t who = __ballot(in);
+        if (!who) continue;
+        const int to = np + lanes_below(who);
+        if (in && to < kPieces) {
+          *reinterpret_cast<v4i*>(held + to * 16) = raw[it];
+          places[to] = (uint16_t)place(it * kVec);
+        }
+        np += __popcll(who);
       }
-      np += __popcll(who);
-    }
-    wave_sync();
-    // Where they do not fit, the lanes with values of at least t are looked at
-    // whole, one after the other; f returns whether to go on.
-    const uint64_t lanes = __ballot(mt >= t);
+      wave_sync();
+      return np;
+    };
+    auto collect_pieces = [&](int np, auto&& wanted) __attribute__((always_inline)) {
+      for (int i = lane; i - lane < np * kVec; i += 64) {
+        const float v = to_float(reinterpret_cast<const T*>(held)[i]);  // of 64 kVec: past np stale ones
+        collect(i < np * kVec && wanted(v), v, places[i / kVec] + i % kVec);
+      }
+    };
+    // The lanes with values of at least t whole, one after the other; f returns
+    // whether to go on.
     auto visit = [&](auto&& f) __attribute__((always_inline)) {
-      for (uint64_t left = lanes; left != 0;) {
+      wave_sync();
+      for (uint64_t left = __ballot(mt >= t); left != 0;) {
         const int slot = lanes_below(left);
         if ((left >> lane & 1) && slot < kHold) {
 #pragma unroll
@@ -346,41 +376,44 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
         wave_sync();
       }
     };
-    if (np <= kPieces) {
-      for (int i = lane; i - lane < np * kVec; i += 64) {
-        const float v = to_float(reinterpret_cast<const T*>(held)[i]);  // of 64 kVec: past np stale ones
-        collect(i < np * kVec && v >= t, v, places[i / kVec] + i % kVec);
-      }
-    } else {
-      visit([&](float v, int at) __attribute__((always_inline)) {
-        collect(v >= t, v, at);
-        return n <= kCand;
-      });
-    }
-    if (n > kCand) {
-      // Many values tie at t: rank the larger ones, mark the tied ones.
-      for (int i = lane; i < kChunk / 32; i += 64) tied[i] = 0;
-      wave_sync();
+    auto reaches = [&](float v) { return v >= t; };
+    auto exceeds = [&](float v) { return v > t; };
+    int np = gather(reaches);
+    if (np <= kPieces) collect_pieces(np, reaches);
+    if (np > kPieces || n > kCand) {
+      // Many values tie at t: rank the larger ones, mark the tied ones, a byte
+      // for each piece.
       n = 0;
-      visit([&](float v, int at) __attribute__((always_inline)) {
-        if (v == t) atomicOr(&tied[at / 32], 1u << (at % 32));
-        collect(v > t, v, at);
-        return n <= kCand;
-      });
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) m |= value(it * kVec + e) == t ? 1u << e : 0u;
+        tied[it * 64 + lane] = (uint8_t)m;
+      }
+      np = gather(exceeds);
+      if (np <= kPieces) {
+        collect_pieces(np, exceeds);
+      } else {
+        visit([&](float v, int at) __attribute__((always_inline)) {
+          collect(v > t, v, at);
+          return n <= kCand;
+        });
+      }
       if (n <= kCand && n < top) {
-        // The first top - n marked values, in order: lane l has kPer words.
-        constexpr int kPer = kChunk / 32 / 64;
+        // The first top - n marked values, in order: lane l has kIter pieces.
         int mine = 0;
-        for (int i = 0; i < kPer; ++i) mine += __popc(tied[lane * kPer + i]);
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) mine += __popc(tied[lane * kIter + i]);
         int pos = mine;
         for (int off = 1; off < 64; off <<= 1) {
           const int o = __shfl_up(pos, off, 64);
           if (lane >= off) pos += o;
         }
         pos += n - mine;
-        for (int i = 0; i < kPer && pos < top; ++i) {
-          for (uint32_t w = tied[lane * kPer + i]; w != 0 && pos < top; w &= w - 1, ++pos)
-            best[pos] = key_of(t, (uint32_t)(base + (lane * kPer + i) * 32 + __ffs((int)w) - 1));
+        for (int i = 0; i < kIter && pos < top; ++i) {
+          for (uint32_t w = tied[lane * kIter + i]; w != 0 && pos < top; w &= w - 1, ++pos)
+            best[pos] = key_of(t, (uint32_t)(base + (lane * kIter + i) * kVec + __ffs((int)w) - 1));
         }
       }
     }
@@ -398,9 +431,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
           if (c < last) k = max_u64(k, c);
           return true;
         });
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) k = max_u64(k, shfl_xor_u64(k, off));
-        last = k;
+        last = wave_max_key(k);
         if (lane == 0) best[r] = last;
       }
     }
@@ -509,8 +540,24 @@ __global__ __launch_bounds__(NT) void logprobs_join_kernel(
     st.S += redS[i];
     st.W += redW[i];
   }
-  if (ncand <= kJoinCand) {
+  if (ncand <= kRankCand || (ncand <= kJoinCand && chunks > 64)) {
     rank_keys<NT>(cand, ncand, top, best);
+  } else if (chunks <= 64 && n <= kJoinCand) {
+    // Many keys near the bound (chunks masked to one value): the chunks' sorted
+    // keys in LDS, merged by one wave with a chunk per lane.
+    __syncthreads();
+    for (int i = threadIdx.x; i < (int)n; i += NT) cand[i] = kr[i];
+    __syncthreads();
+    if (wave == 0) {
+      int at = lane * top, left = lane < chunks ? top : 0;
+      uint64_t head = left > 0 ? cand[at] : 0;
+      for (int r = 0; r < top; ++r) {
+        const uint64_t k = wave_max_key(head);
+        if (lane == 0) best[r] = k;
+        if (k == 0) break;  // best is 0 from here on
+        if (head == k) head = --left > 0 ? cand[++at] : 0;
+      }
+    }
   } else {
     uint64_t last = ~0ull;
     for (int r = 0; r < top && last != 0; ++r) {

@@ -121,6 +121,27 @@ def test_ties(v, kind):
     check(tensor(z, kind), rng.integers(0, v, (8, 1)), 32)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("v", [4000, 21000])
+def test_large_values_in_few_lanes(v, kind):
+    """Large values that fall to a few lanes of a wave only: too many of their pieces, or too many values, for the
+    places they are collected in."""
+    rng = np.random.default_rng(v + 13)
+    i = np.arange(v)
+    for vec in (4, 8):
+        lane = i // vec % 64
+        z = rng.permutation(v)[None, :].repeat(6, 0) / v * 2
+        z[0, lane < 20] += 8                          # 20 lanes, all of their values
+        z[1, (lane < 10) & (i % vec == 1)] += 8       # 10 lanes, a value per piece
+        z[2, lane < 31] += 8
+        z[3] = -65504
+        z[3, lane < 3] = rng.integers(0, 4, (lane < 3).sum())
+        z[4] = np.where(lane < 12, 8 - lane / 8, 0)   # ties within and over the lanes
+        z[5] = np.where((lane < 20) & (i % vec == 0), 3, -np.inf)
+        check(tensor(z, kind), rng.integers(0, v, (6, 1)), 32)
+        check(tensor(z, kind), rng.integers(0, v, (6, 1)), 11)
+
+
 def test_large_values_and_peaked_rows():
     rng = np.random.default_rng(4)
     v = 20000
