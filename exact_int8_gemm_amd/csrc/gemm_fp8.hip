@@ -376,12 +376,16 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   const uint32_t cb0 = (uint32_t)(((lane & 7) ^ swz_b(brow + (lane >> 3))) * 16);
   const uint32_t cb1 = (uint32_t)(((lane & 7) ^ swz_b(brow + 8 * NW + (lane >> 3))) * 16);
   const uint32_t xoff = (uint32_t)((lane >> 3) * K) + ca, woff = (uint32_t)((lane >> 3) * K);
+  // Addresses are computed at each use where registers are short, and held over
+  // the loop by the short tiles (500 x 2560 x 9600 bf16 29.6 -> 27.2 us, 128 x 5120
+  // x 5120 14.7 -> 13.8).
+  auto each_time = [](uint32_t v) __attribute__((always_inline)) { return TM > 2 ? fresh(v) : v; };
   // Rows past M or N lie past their buffer's end and chunks past K are sent
   // there: both read zeros.
   auto copy_x = [&](int c, int b, int buf) __attribute__((always_inline)) {  // c = V pair + v
     const uint32_t ck = (uint32_t)b * kBlock;
     const int row = arow + 16 * TM * (c % V) + 32 * (c / V);
-    const uint32_t in = fresh(xoff) + ((uint32_t)(row * K) + ck);
+    const uint32_t in = each_time(xoff) + ((uint32_t)(row * K) + ck);
     const uint32_t o = ca + ck < (uint32_t)K ? in : kOutOfRange;
     tiled::dma::copy_to_lds(ra, lx0 + (uint32_t)(buf * kXBuf + row * kBlock), o);
   };
@@ -389,7 +393,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
     const uint32_t ck = (uint32_t)b * kBlock;
     const int row = brow + 8 * NW * i;
     const uint32_t cb = NW == 4 && i % 2 == 1 ? cb1 : cb0;
-    const uint32_t in = fresh(woff) + cb + ((uint32_t)(row * K) + ck);
+    const uint32_t in = each_time(woff) + cb + ((uint32_t)(row * K) + ck);
     const uint32_t o = cb + ck < (uint32_t)K ? in : kOutOfRange;
     tiled::dma::copy_to_lds(rb, lw0 + (uint32_t)(buf * kWBuf + row * kBlock), o);
   };
@@ -419,7 +423,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   };
   auto read_w = [&](int buf, int j) __attribute__((always_inline)) {
     const int8_t* p = lw + buf * kWBuf + j * 4 * kBlock;
-    const int wat = (int)fresh((uint32_t)wat0);
+    const int wat = (int)each_time((uint32_t)wat0);
     return Frag16{*reinterpret_cast<const v4i*>(p + wat), *reinterpret_cast<const v4i*>(p + (wat ^ 64))};
   };
   auto read_s = [&](int buf, int i) __attribute__((always_inline)) { return lsa[buf * kScales + xrow + 16 * i]; };
@@ -431,6 +435,11 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   constexpr int kPerP = (nP + 2 * TN - 1) / (2 * TN);                         // copies per MFMA
   constexpr int kPerQ = HAS_Q ? (nQ + kP - kQ - 1) / (kP > kQ ? kP - kQ : 1) : 1;
   constexpr int kLag = 3;
+  // The next weight scale is loaded behind P's reads, whose wait covers it;
+  // before P, P would wait for it (us: 8192 x 5120 x 5120 bf16 187 -> 181, 128 x
+  // 5120 x 5120 fp32 22.1 -> 21.2).  The large fp32 tile is not held up there (768 x
+  // 5120 x 5120 50.7, behind P 52.2).
+  constexpr bool kLateScale = !EXACT || !HAS_Q;
   auto tile = [](int t) { return t < kP ? t / TN : TM - 2 + (t - kP) % 2; };
   auto col = [](int t) { return t < kP ? t % TN : (t - kP) / 2; };
   v4f f[kT], p[kLag];
@@ -452,7 +461,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
     // Weight scale, read a stage ahead (past a select, since a branch would
     // split the loop body) and kept scalar.
     const float sw = uniform(b < KB ? sw_next : 0.0f);
-    sw_next = swp[min(b + 1, KB - 1)];
+    if (!kLateScale) sw_next = swp[min(b + 1, KB - 1)];
     Operand16<EXACT> wo[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) wo[j] = Operand16<EXACT>(wf[j]);
@@ -484,6 +493,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
         sa[a] = read_s(bufn, a);
       }
       if (t >= kP && (t - kP) % 2 == 1) wnext[j] = read_w(bufn, j);
+      if (kLateScale && t == kP + 1) sw_next = swp[min(b + 1, KB - 1)];
       if (t >= kP) {
 #pragma unroll
         for (int c = (t - kP) * kPerP; c < (t - kP + 1) * kPerP; ++c)
