@@ -325,8 +325,13 @@ void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, con
 template <int WN, int TM, int TN, int R>
 constexpr int kTileLds = R * ((32 * TM + 16 * TN * WN) * kBlock + 128 * WN * 4);  // R stages
 
+// Bytes of a row of codes in front of it in its cache line.
+__device__ inline uint32_t line_start(const uint8_t* base, int row, int K) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(base) + (uint64_t)row * (uint64_t)K) % kBlock;
+}
+
 // The tile of BM rows from m0 and BN columns from n0.
-template <typename OUT, bool EXACT, int WN, int TM, int TN, int R>
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, bool LINES>
 __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, const uint8_t* __restrict__ q,
                                                                 const float* __restrict__ s_a,
                                                                 const uint8_t* __restrict__ w,
@@ -372,9 +377,25 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   // is the same in all its activation copies (weights: of each parity).
   const int arow = (wave >> 2) * 16 * TM + (wave & 3) * 8;  // + 16 TM v + 32 pair
   const int brow = wave * 8;                                // + 8 NW i
-  const uint32_t ca = (uint32_t)(((lane & 7) ^ swz_a((wave & 3) * 8 + (lane >> 3))) * 16);
-  const uint32_t cb0 = (uint32_t)(((lane & 7) ^ swz_b(brow + (lane >> 3))) * 16);
-  const uint32_t cb1 = (uint32_t)(((lane & 7) ^ swz_b(brow + 8 * NW + (lane >> 3))) * 16);
+  // LINES: a row starts anywhere, and what is copied of it for a stage is not
+  // the stage's block but the cache line of its number, counted from the line in
+  // which the row starts: one request each, where a block that begins inside a
+  // line would be two.  Block b then lies in lines b and b + 1.  The start within
+  // the line is that of every eighth row.
+  static_assert(!LINES || (TM == 2 && TN == 2 && R >= 4), "two lines are read, R - 3 are on their way");
+  const uint32_t ox = LINES ? line_start(q, m0 + (lane >> 3), K) : 0;
+  const uint32_t ow = LINES ? line_start(w, n0 + (lane >> 3), K) : 0;
+  // A lane's source chunk, k - 128 stage of its row (LINES: before the row's
+  // start it wraps, past K like the others).  LINES: chunk c of a block, and of
+  // the line that holds it, lies at chunk (c + swz) % 8, which reads as free of
+  // conflicts as c ^ swz does.
+  auto source = [&](int swz, uint32_t start) __attribute__((always_inline)) {
+    const int to = lane & 7;
+    return LINES ? (uint32_t)((to + (int)(start / 16) - swz) & 7) * 16 - start : (uint32_t)((to ^ swz) * 16);
+  };
+  const uint32_t ca = source(swz_a((wave & 3) * 8 + (lane >> 3)), ox);
+  const uint32_t cb0 = source(swz_b(brow + (lane >> 3)), ow);
+  const uint32_t cb1 = source(swz_b(brow + 8 * NW + (lane >> 3)), ow);
   const uint32_t xoff = (uint32_t)((lane >> 3) * K) + ca, woff = (uint32_t)((lane >> 3) * K);
   // Addresses are computed at each use where registers are short, and held over
   // the loop by the short tiles (500 x 2560 x 9600 bf16 29.6 -> 27.2 us, 128 x 5120
@@ -417,11 +438,41 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   const int wrow = wn * 16 * TN + 4 * TN * (r >> 2) + (r & 3);
   const int xat = xrow * kBlock + ((g ^ swz_a(xrow)) * 16);
   const int wat0 = wrow * kBlock + ((g ^ swz_b(wrow)) * 16);
+  // LINES: of this lane's chunks g and g + 4, those past the line that the block
+  // begins in are in the next buffer.
+  struct Where {
+    int at[2];
+    bool next[2];
+  };
+  auto where = [&](int row, int swz, uint32_t start) __attribute__((always_inline)) {
+    Where v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      v.at[h] = row * kBlock + ((g + 4 * h + swz) & 7) * 16;
+      v.next[h] = (int)(start / 16) + g + 4 * h >= 8;
+    }
+    return v;
+  };
+  Where xwhere, wwhere[TN];
+  if constexpr (LINES) {
+    xwhere = where(xrow, swz_a(xrow), line_start(q, m0 + xrow, K));
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+      wwhere[j] = where(wrow + 4 * j, swz_b(wrow + 4 * j), line_start(w, n0 + wrow + 4 * j, K));
+  }
+  auto after = [](int buf) __attribute__((always_inline)) { return buf + 1 == R ? 0 : buf + 1; };
+  auto read_lines = [&](const int8_t* p, int size, const Where& v, int buf) __attribute__((always_inline)) {
+    const int a = buf * size, b = after(buf) * size;
+    return Frag16{*reinterpret_cast<const v4i*>(p + (v.next[0] ? b : a) + v.at[0]),
+                  *reinterpret_cast<const v4i*>(p + (v.next[1] ? b : a) + v.at[1])};
+  };
   auto read_x = [&](int buf, int i) __attribute__((always_inline)) {
+    if constexpr (LINES) return read_lines(lx + i * 16 * kBlock, kXBuf, xwhere, buf);
     const int8_t* p = lx + buf * kXBuf + i * 16 * kBlock;
     return Frag16{*reinterpret_cast<const v4i*>(p + xat), *reinterpret_cast<const v4i*>(p + (xat ^ 64))};
   };
   auto read_w = [&](int buf, int j) __attribute__((always_inline)) {
+    if constexpr (LINES) return read_lines(lw, kWBuf, wwhere[j], buf);
     const int8_t* p = lw + buf * kWBuf + j * 4 * kBlock;
     const int wat = (int)each_time((uint32_t)wat0);
     return Frag16{*reinterpret_cast<const v4i*>(p + wat), *reinterpret_cast<const v4i*>(p + (wat ^ 64))};
@@ -479,7 +530,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
       __builtin_amdgcn_sched_barrier(0);
       if (t == kP || (HAS_Q && t == kQ)) {
         wait_lgkm0();  // this wave's reads of what is handed back
-        if (t == kP) tiled::dma::wait_vmcnt<(R - 2) * (nQ + nP) + (HAS_Q ? nQ + nP - 1 : 0)>();
+        if (t == kP) tiled::dma::wait_vmcnt<(R - 2 - LINES) * (nQ + nP) + (HAS_Q ? nQ + nP - 1 : 0)>();
         else tiled::dma::wait_vmcnt<(R - 1) * (nQ + nP)>();
         barrier();
       }
@@ -525,7 +576,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
 #pragma unroll
     for (int c = 0; c < nP; ++c) copy_behind_p(c, b, b);
   }
-  tiled::dma::wait_vmcnt<(R - 1) * (nQ + nP)>();
+  tiled::dma::wait_vmcnt<(R - 1 - LINES) * (nQ + nP)>();
   barrier();
   Frag16 w0[TN], w1[TN];
 #pragma unroll
@@ -603,7 +654,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
 // launch whose tiles do not fill its last round of compute units takes a whole
 // round for them otherwise (2048 x 17408: 544 tiles on 256 CUs are 3 rounds,
 // 512 and 32 x 4 quarters little more than 2).
-template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int RT, int OCC>
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int RT, int OCC, bool LINES>
 __global__ __launch_bounds__(128 * WN, OCC) void gemm_fp8_tile_kernel(const uint8_t* __restrict__ q,
                                                                       const float* __restrict__ s_a,
                                                                       const uint8_t* __restrict__ w,
@@ -619,25 +670,25 @@ __global__ __launch_bounds__(128 * WN, OCC) void gemm_fp8_tile_kernel(const uint
   if (b < full) {
     int tm, tn;
     tile_of(xcd_order(b, full), tiles_m, tiles_n, tm, tn);
-    tile_body<OUT, EXACT, WN, TM, TN, R>(lds, q, s_a, w, s_w, y, M, N, K, tm * 32 * TM, tn * 16 * TN * WN);
+    tile_body<OUT, EXACT, WN, TM, TN, R, LINES>(lds, q, s_a, w, s_w, y, M, N, K, tm * 32 * TM, tn * 16 * TN * WN);
   } else if constexpr (TAIL < TM) {
     constexpr int S = TM / TAIL;
     int tm, tn;
     const int id = xcd_order(b - full, (int)gridDim.x - full);
     tile_of(full + id / S, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * 32 * TM + id % S * 32 * TAIL;
-    if (m0 < M) tile_body<OUT, EXACT, WN, TAIL, TN, RT>(lds, q, s_a, w, s_w, y, M, N, K, m0, tn * 16 * TN * WN);
+    if (m0 < M) tile_body<OUT, EXACT, WN, TAIL, TN, RT, false>(lds, q, s_a, w, s_w, y, M, N, K, m0, tn * 16 * TN * WN);
   }
 }
 
-template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int RT, int OCC>
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int RT, int OCC, bool LINES = false>
 void launch_tile(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
                  int full, hipStream_t st) {
   constexpr int BM = 32 * TM, BN = 16 * TN * WN;
   const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
   const int tiles = tiles_m * tiles_n;
   const int grid = full + (tiles - full) * (TM / TAIL);
-  gemm_fp8_tile_kernel<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC><<<(unsigned)grid, 128 * WN, 0, st>>>(
+  gemm_fp8_tile_kernel<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC, LINES><<<(unsigned)grid, 128 * WN, 0, st>>>(
       q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K, tiles_m, tiles_n, full);
 }
 
@@ -674,14 +725,26 @@ int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_
   }
   const int64_t t64 = tiles(64, 64), t128 = tiles(128, 128), rest = t128 % (2 * kCus);
   const float c128 = (float)(t128 / (2 * kCus)) + (rest == 0 ? 0.0f : rest <= kCus ? 0.66f : 1.0f);
+  // Rows that do not all start on a cache line: the short tiles' own form, with
+  // operands from HBM (us: 500 x 2560 x 9680 48.1 -> 37.0, 1000 x 1300 x 5104 20.9
+  // -> 20.0; from the cache behind the L2s 34.2 and 34.5, 20.9 and 20.8).  Short K
+  // does not pay for its longer ring (300 x 1300 x 2064 7.4, 8.2 so), nor does an
+  // fp32 y, which is bound elsewhere (128 x 5120 x 5104 21.0 and 22.4).
+  const bool lines = K >= 4096 && (K % kBlock != 0 || reinterpret_cast<uintptr_t>(q) % kBlock != 0 ||
+                                   reinterpret_cast<uintptr_t>(w) % kBlock != 0);
+#define PRISM_FP8_SHORT(WN, OCC, FULL)                                                                    \
+  if (lines)                                                                                              \
+    launch_tile<OUT, EXACT, WN, 2, 2, 4, 2, 4, 1, true>(q, s_a, w, s_w, y, M, N, K, (int)(FULL), st);     \
+  else                                                                                                    \
+    PRISM_FP8_TILE(WN, 2, 2, 3, 2, 3, OCC, FULL)
   if constexpr (EXACT) {
     const float c64 = 0.12f + 0.165f * (float)((t64 + kCus - 1) / kCus);
     if (c64 < c128) PRISM_FP8_TILE(2, 2, 2, 3, 2, 3, 3, t64);
     else PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, t128);
   } else if (t64 <= kCus) {
-    PRISM_FP8_TILE(2, 2, 2, 3, 2, 3, 3, t64);
+    PRISM_FP8_SHORT(2, 3, t64);
   } else if (tiles(64, 128) <= kCus) {
-    PRISM_FP8_TILE(4, 2, 2, 3, 2, 3, 2, tiles(64, 128));
+    PRISM_FP8_SHORT(4, 2, tiles(64, 128));
   } else {
     const int64_t t256 = tiles(256, 256), last = t256 % kCus;
     const float c256 = (float)(t256 / kCus) + (last == 0 ? 0.0f : 2 * last <= kCus ? 0.6f : 1.0f);
@@ -690,6 +753,7 @@ int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_
     else if (c192 < c256) PRISM_FP8_TILE(4, 6, 4, 2, 6, 2, 1, tiles(192, 256));
     else PRISM_FP8_TILE(4, 8, 4, 2, 4, 2, 1, 2 * last <= kCus ? t256 - last : t256);
   }
+#undef PRISM_FP8_SHORT
 #undef PRISM_FP8_TILE
   return launch_status();
 }

@@ -385,6 +385,25 @@ def test_gemm_unaligned_16_bit_output():
         check_gemm(q, sa, w, sw, "bf16", y)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,n,k", [(100, 320, 128), (100, 320, 16), (70, 200, 1280), (300, 2100, 400), (1, 300, 640),
+                                   (100, 320, 4096), (70, 200, 4112), (300, 2100, 5104), (130, 3900, 4240)])
+def test_gemm_operands_anywhere_in_a_cache_line(m, n, k, kind):
+    """Codes that start at any 16 bytes: the same bits as aligned ones."""
+    q, sa, w, sw = gemm_input(np.random.default_rng(m + k), m, n, k)
+    want = bits(run_gemm(q, sa, w, sw, kind))
+    qd, wd = as_fp8(q).view(torch.uint8), as_fp8(w).view(torch.uint8)
+    sad, swd = torch.from_numpy(sa).to(DEV), torch.from_numpy(sw).to(DEV)
+    for oq, ow in ((16, 0), (0, 112), (48, 80), (112, 112)):
+        bq = torch.full((m * k + 256,), 0x7F, dtype=torch.uint8, device=DEV)  # NaN codes around them
+        bw = torch.full((n * k + 256,), 0x7F, dtype=torch.uint8, device=DEV)
+        q1, w1 = bq[oq:oq + m * k].view(m, k), bw[ow:ow + n * k].view(n, k)
+        q1.copy_(qd)
+        w1.copy_(wd)
+        y = prism.gemm_fp8_blockscale(q1.view(prism.FP8), sad, w1.view(prism.FP8), swd, out_dtype=TYPES[kind])
+        assert torch.equal(bits(y), want), (oq, ow)
+
+
 def test_gemm_outputs_past_32_bit_offsets():
     """More than 2^31 outputs: the last rows are the rows of a small call."""
     m, n, k = 131200, 16500, 16
