@@ -307,8 +307,8 @@ void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, con
 // taken away, the kernels take the same time).
 //
 // What bounds the 256 x 256 form, MI355X, M = N = K = 8192 (480-510 us, 2.2
-// PFLOP/s; 8192 x 5120 x 5120: 195 us, 2.2 PFLOP/s): the matrix cores are busy
-// 58% of the cycles at a clock that the power limit holds at 1.9 GHz; without
+// PFLOP/s; 8192 x 5120 x 5120: 181 to 193 us, 2.3 PFLOP/s): the matrix cores are
+// busy 58% of the cycles at a clock that the power limit holds at 1.9 GHz; without
 // the copies it takes 423 us, without the LDS reads 416, without the folds
 // 405, without either barrier 465.  Times of these parts add up rather than
 // hide behind each other, because each costs clock.  Other forms measured and
@@ -316,12 +316,14 @@ void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, con
 // issued together (265 against 225 us at 8192 x 5120 x 5120), one barrier per
 // stage (4% slower), 128 x 128 tiles of four waves (twice the copies: 560 us).
 //
-// The smaller forms are bound by their copies, 20 to 33 bytes a clock and CU
-// whatever R is (500 x 2560 x 9680, 160 tiles of 64 x 128: 34 us with inputs in
-// the cache behind the L2s, 47 from HBM, where rows that start inside a cache
-// line cost two requests a copy: 31 at K = 9600).  The fp32 form, 128 x 128, is
-// bound by the f16 MFMAs and the conversions (8192 x 5120 x 5120: 381 us, 53%
-// busy; 305 at the rate of a large 16-bit library product).
+// The smaller forms are bound by a stage's chain of copies, barrier, LDS reads
+// and MFMAs, whatever R is (500 x 2560 x 9600, 160 tiles of 64 x 128: 27 to 32
+// us, 36 from HBM; in one run of 32 us, without copies 21, without LDS reads 28,
+// without the barrier 29, without all three 15).  The fp32 form, 128 x 128, is
+// bound by the f16 MFMAs and the conversions, which share a SIMD's issue (8192 x
+// 5120 x 5120: 373 to 385 us, MFMAs 52% busy; 305 at the rate of a large 16-bit
+// library product).  Spread between the MFMAs, the conversions took 4% fewer
+// cycles and the same time, at a lower clock.
 template <int WN, int TM, int TN, int R>
 constexpr int kTileLds = R * ((32 * TM + 16 * TN * WN) * kBlock + 128 * WN * 4);  // R stages
 
@@ -387,8 +389,8 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   const uint32_t ow = LINES ? line_start(w, n0 + (lane >> 3), K) : 0;
   // A lane's source chunk, k - 128 stage of its row (LINES: before the row's
   // start it wraps, past K like the others).  LINES: chunk c of a block, and of
-  // the line that holds it, lies at chunk (c + swz) % 8, which reads as free of
-  // conflicts as c ^ swz does.
+  // the line that holds it, lies at chunk (c + swz) % 8 (128 x 5120 x 5104: 15.1 us,
+  // at c ^ swz 15.9).
   auto source = [&](int swz, uint32_t start) __attribute__((always_inline)) {
     const int to = lane & 7;
     return LINES ? (uint32_t)((to + (int)(start / 16) - swz) & 7) * 16 - start : (uint32_t)((to ^ swz) * 16);
@@ -703,7 +705,7 @@ constexpr int kCus = 256;
 //    (5120 x 5120, M = 64: 18.5 against 22.5);
 //  * 16-bit y: 64 x 64 tiles while they fit the CUs at once (128 x 5120 x 5120:
 //    15.1, 64 x 128 tiles 18.2), 64 x 128 tiles while those do (500 x 2560 x
-//    9680: 34.9, 64 x 64 40.6, 128 x 128 47), else the smallest estimate of
+//    9680: 33.7, 64 x 64 40.6, 128 x 128 47), else the smallest estimate of
 //    128 x 128, 192 x 256 and 256 x 256 tiles (K = 5120: 768 x 5120 32.8, 58.3
 //    and 44.2; 2048 x 5120 73.6, 61.2 and 65.2; 1536 x 9728 94, 110 and 71);
 //  * fp32 y, bound by the MFMAs and conversions of a wave: the smaller estimate
