@@ -48,7 +48,9 @@ constexpr float kNegInf = -__builtin_inff();
 // Lowest exponent of 2 taken: 2^-200 is 0 in fp32, and unlike -inf it can be
 // multiplied by that.
 constexpr float kFloor = -200.0f;
-constexpr float kLargest = 1e30f;
+// Largest |m| of a chunk whose terms take one fma each: the rounding of m
+// log2(e), by which all their exponents are off, is at most 2^-4.
+constexpr float kOneFma = 0x1p20f;
 
 struct Stats {
   float m, S, W;
@@ -294,10 +296,11 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
   st.m = wave_max(mt);
   const float b = base_of(st.m);
   float S = 0.0f, W = 0.0f;  // W in powers of 2
-  if (fabsf(b) < kLargest) {
+  if (fabsf(b) < kOneFma) {
     // (v - b) log2(e) as one fma: v L - c with c = fl(b L).  Every term is then
     // 2^d too large for d = b L - c, which an fma gives exactly: taken out of
-    // the sums below.
+    // the sums below.  |d| is up to half a step of c, 2^-4 here; without a bound
+    // on b, 2^d leaves fp32 from |b| = 1.5e9 on.
     const float c = b * kLog2E, d = __builtin_fmaf(b, kLog2E, -c);
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
     const float x = __builtin_amdgcn_exp2f(-d);
     S *= x;
     W = __builtin_fmaf(W, x, -d * S);
-  } else {  // b L may overflow (a NaN also comes here)
+  } else {  // chunks masked to one finite value, mostly (a NaN also comes here)
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
       const float t = log2_term(value(i) - b);

@@ -220,3 +220,37 @@ def test_logits_past_32_bit_offsets():
     assert abs(float(r.lse[0]) - np.log(v)) < 1e-4 and abs(float(r.entropy[0]) - np.log(v)) < 1e-3
     del z
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("mask", [-1e5, -2.0 ** 20, -1e9, -2e9, -1e10, -1e12, -1e20, -9e29, -1e30, -1e38])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("v,top", [(3000, 7), (20011, 0), (20011, 6), (100003, 20), (300000, 3)])
+def test_finite_masks_of_any_size(v, top, kind, mask):
+    """Logits masked by a finite value: a few tokens left, spread out, in the first or in the last values only (whole
+    chunks of 4096 and a cut last one have nothing but the mask), and none."""
+    rng = np.random.default_rng(v + top)
+    z = 2 * rng.standard_normal((5, v))
+    z[0, rng.random(v) < 0.99] = mask
+    z[1, 100:] = mask
+    z[2, :v - 50] = mask
+    z[3] = mask
+    z[4, v // 2] = mask
+    check(tensor(z, kind), rng.integers(0, v, (5, 3)), top)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("v", [50, 4096, 9000])
+def test_rows_of_any_magnitude(v, kind):
+    """Uniform rows, rows a few logits wide where the type holds them, and rows spread over their magnitude, of both
+    signs and every power of ten, and at 2^20 and its neighbours."""
+    rng = np.random.default_rng(v + 17)
+    near = [2.0 ** 20, np.nextafter(np.float32(2.0 ** 20), np.float32(0)), 2.0 ** 20 + 0.125, 2.0 ** 20 * 1.0078125]
+    sizes = [10.0 ** k for k in range(3, 39)] + [float(x) for x in near] + [1.5e9, 1.7e9, 3e9, 7e9, 0.99e30]
+    rows = []
+    for b in sizes:
+        for sign in (1, -1):
+            rows.append(np.full(v, sign * b))
+            rows.append(sign * b - 12 * rng.random(v))
+            rows.append(sign * b * rng.uniform(0.4, 1, v))
+    z = np.stack(rows)
+    check(tensor(z, kind), rng.integers(0, v, (len(z), 2)), 5)
