@@ -512,8 +512,8 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   // Stage b in buffer buf, the next one in bufn (constants where R = 2).
   auto stage = [&](int b, const int buf, const int bufn, const Frag16* wf, Frag16* wnext) __attribute__((always_inline)) {
     // Weight scale, read a stage ahead (past a select, since a branch would
-    // split the loop body) and kept scalar.
-    const float sw = uniform(b < KB ? sw_next : 0.0f);
+    // split the loop body) and kept scalar; -0 past K, see below.
+    const float sw = uniform(b < KB ? sw_next : -0.0f);
     if (!kLateScale) sw_next = swp[min(b + 1, KB - 1)];
     Operand16<EXACT> wo[TN];
 #pragma unroll
@@ -588,8 +588,9 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   }
 #pragma unroll
   for (int j = 0; j < TN; ++j) w0[j] = read_w(0, j);
-  // Two stages per turn; a stage past K multiplies zeros by scales 0 and
-  // leaves f as it is (f starts at +0 and is never -0).
+  // Two stages per turn; a stage past K has P = +0 from zero codes and the scale
+  // +0 * -0, so its fold adds -0, which leaves any f as it is: also a -0, to
+  // which a negative sum below fp32 rounds and which +0 would make a +0.
   if constexpr (R == 2) {
     for (int b = 0; b < KB; b += 2) {
       stage(b, 0, 1, w0, w1);

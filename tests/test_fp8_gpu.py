@@ -579,3 +579,24 @@ def test_empty_batches():
     assert prism.swiglu_quantize_fp8(torch.empty((0, 32), device=DEV), torch.empty((0, 32), device=DEV))[0].shape == (0, 32)
     r = prism.token_logprobs(torch.empty((0, 50), device=DEV), top=4)
     assert r.lse.shape == (0,) and r.top_ids.shape == (0, 4)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("k", [128, 256, 384, 5104, 5120, 5248])
+def test_gemm_zeros_keep_their_sign_in_any_batch(k, kind):
+    """Products that fall below fp32: a sum of a negative one is -0 by the chain's definition, in every kernel form
+    and whatever number of blocks the form walks."""
+    n = 300
+    q = np.zeros((600, k))
+    w = np.zeros((n, k))
+    q[::2, k - 1] = 2.0 ** -9         # the last block's only product; the blocks before it add +0 to +0
+    w[:, k - 1] = np.where(np.arange(n) % 3 == 0, 2.0 ** -9, -(2.0 ** -9))
+    kb = -(-k // 128)
+    sa = np.full((kb, 600), np.float32(2.0 ** -70))
+    sw = np.full((-(-n // 128), kb), np.float32(2.0 ** -70))
+    # +-2^-18 * 2^-140 rounds to +-0; the odd rows' products are +0 * 2^-140
+    want = np.where((np.arange(600)[:, None] % 2 == 0) & (w[:, k - 1] < 0), np.float32(-0.0), np.float32(0.0))
+    want = bits(torch.from_numpy(want).to(TYPES[kind]))
+    for m in (1, 4, 16, 32, 64, 100, 300, 600):
+        y = run_gemm(q[:m], np.ascontiguousarray(sa[:, :m]), w, sw, kind)
+        assert torch.equal(bits(y).cpu(), want[:m]), m
