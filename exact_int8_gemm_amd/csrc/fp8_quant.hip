@@ -25,15 +25,16 @@ __device__ inline uint32_t max16(uint32_t m) {
   return m;
 }
 
-// h = g / (1 + exp(-g)) * u as (g / 16) * (1 / (1 / 16 + exp(-g) / 16)) * u:
-// the reciprocal is v_rcp_f32 (1 ulp), and the 16 keeps it a normal number
-// down to g = -90; below it is 0.  exp's argument is one fma with the rounding
+// h = g / (1 + exp(-g)) * u as (1 / (1 / 16 + exp(-g) / 16) / 16) * g * u: the
+// reciprocal is v_rcp_f32 (1 ulp), and the 16 keeps it a normal number down to
+// g = -90; below it is 0.  It is scaled back before g is multiplied in, so that
+// a subnormal gate keeps its bits.  exp's argument is one fma with the rounding
 // of fp32, |g| 2^-24 relative (5e-6 at g = -80).  All of it is four orders
 // below a code's half step, and an IEEE division would be a third of the
 // kernel's instructions (2048 x 17360 bf16: 42.3 us).
 __device__ inline float swiglu(float g, float u) {
   const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(g, -0x1.715476p+0f, -4.0f));
-  return g * 0x1p-4f * __builtin_amdgcn_rcpf(e + 0x1p-4f) * u;
+  return __builtin_amdgcn_rcpf(e + 0x1p-4f) * 0x1p-4f * g * u;
 }
 
 // One 16-lane group per 1 x 128 block and step; a workgroup takes 16 rows by

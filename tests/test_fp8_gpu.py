@@ -600,3 +600,21 @@ def test_gemm_zeros_keep_their_sign_in_any_batch(k, kind):
     for m in (1, 4, 16, 32, 64, 100, 300, 600):
         y = run_gemm(q[:m], np.ascontiguousarray(sa[:, :m]), w, sw, kind)
         assert torch.equal(bits(y).cpu(), want[:m]), m
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_swiglu_of_tiny_gates(kind):
+    """Subnormal gates and large factors: h = gate / 2 * up, exact in fp32 for even multiples of the smallest gate."""
+    step = 2.0 ** -149 if kind == "f32" else 2.0 ** -133
+    g = torch.from_numpy((np.arange(2, 258, 2) * step * np.where(np.arange(128) % 3, 1, -1))[None].repeat(3, 0).astype(np.float32))
+    g = g.to(TYPES[kind]).to(DEV)
+    u = torch.full((3, 128), 2.0 ** 100, device=DEV)
+    u[1] *= -3
+    u[2, ::2] = 2.0 ** 90
+    u = u.to(TYPES[kind])
+    q, s = prism.swiglu_quantize_fp8(g, u)
+    h = host(g).astype(np.float64) / 2 * host(u)
+    assert np.allclose(host(s), np.abs(h).max(1) / 448, rtol=2.0 ** -17, atol=0)
+    lo, hi = swiglu_bounds(h, host(s), 128)
+    got = host(q)
+    assert ((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi))).all()
