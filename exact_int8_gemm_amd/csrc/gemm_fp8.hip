@@ -10,15 +10,17 @@
 // kernels give a row the same bits.
 //
 // Which instructions depends on y's type.  v_mfma_f32_16x16x128_f8f6f4 aligns
-// its products to their largest before it adds them: measured on MI355X
-// against 64-bit sums, its error reaches 2^-10.9 of the largest product of the
-// block (2-norm over N(0, 1) operands: 1.4e-5; with one activation per block
-// 50 times the others: 3.8e-5).  That is below the rounding of a 16-bit y
-// (bf16 1.7e-3, f16 2.1e-4) and of the codes themselves (2^-4), but not what
-// an fp32 y promises.  So 16-bit outputs take that instruction, and an fp32 y
-// takes four v_mfma_f32_16x16x32_f16 on the codes converted to f16 in
-// registers: every e4m3 value and product is exact there, and the error is
-// that of fp32 sums (2-norm 1e-8), at half the matrix rate.
+// each eight products of consecutive k to the largest exponent among them and
+// cuts what lies 2^-13 below it (found on MI355X with one large product and
+// seven small ones at every place).  So products of one sign lose at most 7 *
+// 2^-13 = 2^-10.2 of their sum, less than a bf16 y's rounding (2^-9 to 2^-8)
+// but more than an f16 y's (2^-12 to 2^-11), and where products cancel the error
+// reaches 112 * 2^-13 = 2^-6.2 of the block's largest (2^-6.4 seen; over N(0, 1)
+// operands 2^-10.9, 2-norm 1.4e-5; with one activation per block 50 times the
+// others 3.8e-5).  bf16 outputs take that instruction.  fp32 and f16 outputs take
+// four v_mfma_f32_16x16x32_f16 on the codes converted to f16 in registers: every
+// e4m3 value and product is exact there, and the error is that of fp32 sums
+// (2-norm 1e-8), at half the matrix rate.
 //
 // Lane layout (both): lane l supplies row l % 16 of either operand; its 32
 // codes of a block are the two 16-byte chunks l / 16 and l / 16 + 4.  The
@@ -702,18 +704,18 @@ constexpr int kCus = 256;
 // below; every choice gives the same bits):
 //  * small kernel: M <= 8; up to 16 rows where N <= 16384 (17408 x 5120, M =
 //    16: 64 x 64 tiles 20.6 against 24.0), up to 32 rows where N <= 6144 (5120
-//    x 5120, M = 32: 11.9 against 15.0), for an fp32 y up to 64 rows there
+//    x 5120, M = 32: 11.9 against 15.0), for an fp32 or f16 y up to 64 rows there
 //    (5120 x 5120, M = 64: 18.5 against 22.5);
-//  * 16-bit y: 64 x 64 tiles while they fit the CUs at once (128 x 5120 x 5120:
+//  * bf16 y: 64 x 64 tiles while they fit the CUs at once (128 x 5120 x 5120:
 //    15.1, 64 x 128 tiles 18.2), 64 x 128 tiles while those do (500 x 2560 x
 //    9680: 33.7, 64 x 64 40.6, 128 x 128 47), else the smallest estimate of
 //    128 x 128, 192 x 256 and 256 x 256 tiles (K = 5120: 768 x 5120 32.8, 58.3
 //    and 44.2; 2048 x 5120 73.6, 61.2 and 65.2; 1536 x 9728 94, 110 and 71);
-//  * fp32 y, bound by the MFMAs and conversions of a wave: the smaller estimate
+//  * fp32 or f16 y, bound by the MFMAs and conversions of a wave: the smaller estimate
 //    of 64 x 64 and 128 x 128 tiles (K = 5120: 1024 x 2560 42.6 and 49.7; 768 x
 //    5120 58.7 and 51.6; 2048 x 5120 135 and 116).
 // An estimate counts rounds of the CUs, relative to a full round of 256 x 256
-// tiles, or with an fp32 y of two 128 x 128 tiles per CU.  One workgroup per CU
+// tiles, or with exact products of two 128 x 128 tiles per CU.  One workgroup per CU
 // of the latter takes two thirds of the time of two; 256 x 256 tiles that fill
 // at most half of their last round are cut in two there, for 0.6 of a round.
 template <typename OUT, bool EXACT>
@@ -732,7 +734,7 @@ int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_
   // operands from HBM (us: 500 x 2560 x 9680 48.1 -> 37.0, 1000 x 1300 x 5104 20.9
   // -> 20.0; from the cache behind the L2s 34.2 and 34.5, 20.9 and 20.8).  Short K
   // does not pay for its longer ring (300 x 1300 x 2064 7.4, 8.2 so), nor does an
-  // fp32 y, which is bound elsewhere (128 x 5120 x 5104 21.0 and 22.4).
+  // exact sum, which is bound elsewhere (128 x 5120 x 5104 21.0 and 22.4).
   const bool lines = K >= 4096 && (K % kBlock != 0 || reinterpret_cast<uintptr_t>(q) % kBlock != 0 ||
                                    reinterpret_cast<uintptr_t>(w) % kBlock != 0);
 #define PRISM_FP8_SHORT(WN, OCC, FULL)                                                                    \
@@ -766,7 +768,7 @@ int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_
 int launch_gemm_fp8(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int type, int M,
                     int N, int K, hipStream_t st) {
   if (type == PRISM_TYPE_F32) return launch<float, true>(q, s_a, w, s_w, y, M, N, K, st);
-  if (type == PRISM_TYPE_F16) return launch<_Float16, false>(q, s_a, w, s_w, y, M, N, K, st);
+  if (type == PRISM_TYPE_F16) return launch<_Float16, true>(q, s_a, w, s_w, y, M, N, K, st);
   return launch<__bf16, false>(q, s_a, w, s_w, y, M, N, K, st);
 }
 

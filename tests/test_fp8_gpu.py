@@ -618,3 +618,55 @@ def test_swiglu_of_tiny_gates(kind):
     lo, hi = swiglu_bounds(h, host(s), 128)
     got = host(q)
     assert ((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi))).all()
+
+
+def eights(place, sign, kind, cut, mantissa):
+    """One product of 2^16 among each eight of a block, at `place`, of alternating signs or of one; the others
+    mantissa^2 2^(16 - cut).  -> q, w of 128."""
+    q = np.full(128, mantissa)
+    w = np.full(128, sign * mantissa * 2.0 ** (16 - cut))
+    q[place::8] = 256
+    w[place::8] = 256
+    if kind == "cancel":
+        w[place::16] = -256
+    return ref.round_e4m3(q), ref.round_e4m3(w)
+
+
+@pytest.mark.parametrize("m", [1, 16, 64, 200])
+@pytest.mark.parametrize("kind", ["cancel", "one sign"])
+def test_gemm_sums_of_large_and_small_products(kind, m):
+    """Sums that lose most where products are cut before they are added.
+
+    fp32 and f16 y: exact products, the tolerance of fp32 sums.  bf16 y: each eight products are aligned to the largest
+    and cut below 2^-13 of its exponent: the 112 others lose at most 112 * 2^-13 of the block's largest product, and
+    of one sign at most 7 * 2^-13 of the sum.  Each with one rounding of y."""
+    pairs = [eights(p, s, kind, cut, man) for p in (0, 3, 7) for s in ((1, -1) if kind == "cancel" else (1,))
+             for cut in range(11, 18) for man in (1.0, 1.875, 1.25)]
+    q = np.stack([a for a, _ in pairs] * -(-m // len(pairs)))[:m]
+    w = np.stack([b for _, b in pairs])
+    n = len(w)
+    take = np.zeros(128)
+    take[:0 if kind == "cancel" else 16] = 256
+    # block 1: nothing, or what takes the large products out of the sum again
+    for second in (0 * take, take):
+        q2 = np.concatenate([q, np.tile(second, (m, 1))], 1)
+        w2 = np.concatenate([w, np.tile(-take, (n, 1))], 1)
+        sa, sw = np.full((2, m), np.float32(2.0 ** -10)), np.ones((-(-n // 128), 2), np.float32)
+        exact, mag = ref.gemm(q2, sa, w2, sw)
+        sums = (128 * 2.0 ** -23 + 4 * 2.0 ** -24) * mag
+        for t in TYPES:
+            y = host(run_gemm(q2, sa, w2, sw, t)).astype(np.float64)
+            tol = sums + EPS[t] / 2 * (np.abs(exact) + sums) + (2.0 ** -25 if t == "f16" else 0)
+            if t == "bf16":
+                cut = 112 * 2.0 ** -13 * 2.0 ** 16 * 2.0 ** -10
+                if kind == "one sign":
+                    cut = np.minimum(cut, 7 * 2.0 ** -13 * 2.0 ** -10 * (np.abs(q) @ np.abs(w).T))
+                tol = tol + cut * (1 + EPS[t])
+            assert (np.abs(y - exact) <= tol).all(), (t, float((np.abs(y - exact) / tol).max()))
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_gemm_fp16_is_fp32_rounded(m, n, k):
+    args = gemm_input(np.random.default_rng(m * 5 + n + k), m, n, k)
+    want = run_gemm(*args, "f32").cpu().half()
+    assert torch.equal(bits(run_gemm(*args, "f16")).cpu(), bits(want))
