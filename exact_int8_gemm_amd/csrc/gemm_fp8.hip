@@ -248,11 +248,33 @@ __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_
   }
 }
 
+// Operands of a call.  With `check` the functions below launch nothing: they
+// only say whether the grid of the kernel that they choose can be launched.
+struct Call {
+  const uint8_t* q;
+  const float* s_a;
+  const uint8_t* w;
+  const float* s_w;
+  void* y;
+  int M, N, K;
+  hipStream_t st;
+  bool check;
+};
+
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A grid has fewer than 2^32 threads.
+int check_grid(int64_t groups, int threads) {
+  return groups * threads <= (int64_t)UINT32_MAX ? PRISM_OK : PRISM_ERR_INVALID_ARG;
+}
+
 template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES>
-void launch_small(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
-                  hipStream_t st) {
-  gemm_fp8_small_kernel<OUT, EXACT, MT, RP, CB, WAVES><<<(unsigned)((N + 16 * CB - 1) / (16 * CB)), 64 * WAVES, 0, st>>>(
-      q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K);
+int launch_small(const Call& c) {
+  const int64_t groups = ceil_div(c.N, 16 * CB);
+  if (c.check) return check_grid(groups, 64 * WAVES);
+  gemm_fp8_small_kernel<OUT, EXACT, MT, RP, CB, WAVES><<<(unsigned)groups, 64 * WAVES, 0, c.st>>>(
+      c.q, c.s_a, c.w, c.s_w, static_cast<OUT*>(c.y), c.M, c.N, c.K);
+  return launch_status();
 }
 
 // Waves and columns per workgroup by N: about 80 to 160 workgroups of eight
@@ -260,23 +282,26 @@ void launch_small(const uint8_t* q, const float* s_a, const uint8_t* w, const fl
 // 2560 x 9728 8.4, 16 columns more 11.8; 5120 x 5120 7.3, 16 columns fewer 8.3),
 // four waves and 16 columns for wide ones (9728 x 2560 6.7, eight waves 8.0).
 template <typename OUT, bool EXACT>
-void launch_small_rows(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N,
-                       int K, hipStream_t st) {
-#define PRISM_FP8_SMALL(MT, RP, CB, WAVES) launch_small<OUT, EXACT, MT, RP, CB, WAVES>(q, s_a, w, s_w, y, M, N, K, st)
-#define PRISM_FP8_SMALL_N(MT, RP)                     \
-  if (N <= 3840) PRISM_FP8_SMALL(MT, RP, 1, 8);       \
-  else if (N <= 8192) PRISM_FP8_SMALL(MT, RP, 2, 8);  \
-  else PRISM_FP8_SMALL(MT, RP, 1, 4)
+int launch_small_rows(const Call& c) {
+  const int M = c.M, N = c.N;
+#define PRISM_FP8_SMALL(MT, RP, CB, WAVES) return launch_small<OUT, EXACT, MT, RP, CB, WAVES>(c)
+#define PRISM_FP8_SMALL_N(MT, RP)                    \
+  if (N <= 3840) PRISM_FP8_SMALL(MT, RP, 1, 8);      \
+  if (N <= 8192) PRISM_FP8_SMALL(MT, RP, 2, 8);      \
+  PRISM_FP8_SMALL(MT, RP, 1, 4)
   if (M <= 4) {
     PRISM_FP8_SMALL_N(1, 4);
-  } else if (M <= 16) {
+  }
+  if (M <= 16) {
     PRISM_FP8_SMALL_N(1, 16);
-  } else if (M <= 32) {  // N <= 6144 from here on
+  }
+  if (M <= 32 || !EXACT) {  // N <= 6144 from here on
     if (N <= 3840) PRISM_FP8_SMALL(2, 16, 1, 8);
-    else PRISM_FP8_SMALL(2, 16, 2, 8);
-  } else if constexpr (EXACT) {
+    PRISM_FP8_SMALL(2, 16, 2, 8);
+  }
+  if constexpr (EXACT) {
     if (N <= 3840) PRISM_FP8_SMALL(4, 16, 1, 8);
-    else PRISM_FP8_SMALL(4, 16, 2, 8);
+    PRISM_FP8_SMALL(4, 16, 2, 8);
   }
 #undef PRISM_FP8_SMALL_N
 #undef PRISM_FP8_SMALL
@@ -687,14 +712,13 @@ __global__ __launch_bounds__(128 * WN, OCC) void gemm_fp8_tile_kernel(const uint
 }
 
 template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int RT, int OCC, bool LINES = false>
-void launch_tile(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
-                 int full, hipStream_t st) {
-  constexpr int BM = 32 * TM, BN = 16 * TN * WN;
-  const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
-  const int tiles = tiles_m * tiles_n;
-  const int grid = full + (tiles - full) * (TM / TAIL);
-  gemm_fp8_tile_kernel<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC, LINES><<<(unsigned)grid, 128 * WN, 0, st>>>(
-      q, s_a, w, s_w, static_cast<OUT*>(y), M, N, K, tiles_m, tiles_n, full);
+int launch_tile(const Call& c, int64_t full) {
+  const int64_t tiles_m = ceil_div(c.M, 32 * TM), tiles_n = ceil_div(c.N, 16 * TN * WN);
+  const int64_t groups = full + (tiles_m * tiles_n - full) * (TM / TAIL);
+  if (c.check) return check_grid(groups, 128 * WN);
+  gemm_fp8_tile_kernel<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC, LINES><<<(unsigned)groups, 128 * WN, 0, c.st>>>(
+      c.q, c.s_a, c.w, c.s_w, static_cast<OUT*>(c.y), c.M, c.N, c.K, (int)tiles_m, (int)tiles_n, (int)full);
+  return launch_status();
 }
 
 // Number of compute units that the choices below count with (MI355X).
@@ -719,15 +743,13 @@ constexpr int kCus = 256;
 // of the latter takes two thirds of the time of two; 256 x 256 tiles that fill
 // at most half of their last round are cut in two there, for 0.6 of a round.
 template <typename OUT, bool EXACT>
-int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int M, int N, int K,
-           hipStream_t st) {
-  auto tiles = [&](int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+int launch(const Call& c) {
+  const int M = c.M, N = c.N, K = c.K;
+  auto tiles = [&](int bm, int bn) { return ceil_div(M, bm) * ceil_div(N, bn); };
 #define PRISM_FP8_TILE(WN, TM, TN, R, TAIL, RT, OCC, FULL) \
-  launch_tile<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC>(q, s_a, w, s_w, y, M, N, K, (int)(FULL), st)
-  if (M <= 8 || (M <= 16 && N <= 16384) || (M <= (EXACT ? 64 : 32) && N <= 6144)) {
-    launch_small_rows<OUT, EXACT>(q, s_a, w, s_w, y, M, N, K, st);
-    return launch_status();
-  }
+  return launch_tile<OUT, EXACT, WN, TM, TN, R, TAIL, RT, OCC>(c, FULL)
+  if (M <= 8 || (M <= 16 && N <= 16384) || (M <= (EXACT ? 64 : 32) && N <= 6144))
+    return launch_small_rows<OUT, EXACT>(c);
   const int64_t t64 = tiles(64, 64), t128 = tiles(128, 128), rest = t128 % (2 * kCus);
   const float c128 = (float)(t128 / (2 * kCus)) + (rest == 0 ? 0.0f : rest <= kCus ? 0.66f : 1.0f);
   // Rows that do not all start on a cache line: the short tiles' own form, with
@@ -735,41 +757,48 @@ int launch(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_
   // -> 20.0; from the cache behind the L2s 34.2 and 34.5, 20.9 and 20.8).  Short K
   // does not pay for its longer ring (300 x 1300 x 2064 7.4, 8.2 so), nor does an
   // exact sum, which is bound elsewhere (128 x 5120 x 5104 21.0 and 22.4).
-  const bool lines = K >= 4096 && (K % kBlock != 0 || reinterpret_cast<uintptr_t>(q) % kBlock != 0 ||
-                                   reinterpret_cast<uintptr_t>(w) % kBlock != 0);
-#define PRISM_FP8_SHORT(WN, OCC, FULL)                                                                    \
-  if (lines)                                                                                              \
-    launch_tile<OUT, EXACT, WN, 2, 2, 4, 2, 4, 1, true>(q, s_a, w, s_w, y, M, N, K, (int)(FULL), st);     \
-  else                                                                                                    \
-    PRISM_FP8_TILE(WN, 2, 2, 3, 2, 3, OCC, FULL)
+  const bool lines = K >= 4096 && (K % kBlock != 0 || reinterpret_cast<uintptr_t>(c.q) % kBlock != 0 ||
+                                   reinterpret_cast<uintptr_t>(c.w) % kBlock != 0);
+#define PRISM_FP8_SHORT(WN, OCC, FULL)                                                 \
+  if (lines) return launch_tile<OUT, EXACT, WN, 2, 2, 4, 2, 4, 1, true>(c, FULL);      \
+  PRISM_FP8_TILE(WN, 2, 2, 3, 2, 3, OCC, FULL)
   if constexpr (EXACT) {
     const float c64 = 0.12f + 0.165f * (float)((t64 + kCus - 1) / kCus);
     if (c64 < c128) PRISM_FP8_TILE(2, 2, 2, 3, 2, 3, 3, t64);
-    else PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, t128);
-  } else if (t64 <= kCus) {
-    PRISM_FP8_SHORT(2, 3, t64);
-  } else if (tiles(64, 128) <= kCus) {
-    PRISM_FP8_SHORT(4, 2, tiles(64, 128));
+    PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, t128);
   } else {
+    if (t64 <= kCus) {
+      PRISM_FP8_SHORT(2, 3, t64);
+    }
+    if (tiles(64, 128) <= kCus) {
+      PRISM_FP8_SHORT(4, 2, tiles(64, 128));
+    }
     const int64_t t256 = tiles(256, 256), last = t256 % kCus;
     const float c256 = (float)(t256 / kCus) + (last == 0 ? 0.0f : 2 * last <= kCus ? 0.6f : 1.0f);
     const float c192 = 0.83f * (float)((tiles(192, 256) + kCus - 1) / kCus);
     if (0.68f * c128 < c192 && 0.68f * c128 < c256) PRISM_FP8_TILE(2, 4, 4, 2, 4, 2, 2, t128);
-    else if (c192 < c256) PRISM_FP8_TILE(4, 6, 4, 2, 6, 2, 1, tiles(192, 256));
-    else PRISM_FP8_TILE(4, 8, 4, 2, 4, 2, 1, 2 * last <= kCus ? t256 - last : t256);
+    if (c192 < c256) PRISM_FP8_TILE(4, 6, 4, 2, 6, 2, 1, tiles(192, 256));
+    PRISM_FP8_TILE(4, 8, 4, 2, 4, 2, 1, 2 * last <= kCus ? t256 - last : t256);
   }
 #undef PRISM_FP8_SHORT
 #undef PRISM_FP8_TILE
-  return launch_status();
+}
+
+int dispatch(const Call& c, int type) {
+  if (type == PRISM_TYPE_F32) return launch<float, true>(c);
+  if (type == PRISM_TYPE_F16) return launch<_Float16, true>(c);
+  return launch<__bf16, false>(c);
 }
 
 }  // namespace
 
+int check_gemm_fp8_grid(const uint8_t* q, const uint8_t* w, int type, int M, int N, int K) {
+  return dispatch({q, nullptr, w, nullptr, nullptr, M, N, K, nullptr, true}, type);
+}
+
 int launch_gemm_fp8(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int type, int M,
                     int N, int K, hipStream_t st) {
-  if (type == PRISM_TYPE_F32) return launch<float, true>(q, s_a, w, s_w, y, M, N, K, st);
-  if (type == PRISM_TYPE_F16) return launch<_Float16, true>(q, s_a, w, s_w, y, M, N, K, st);
-  return launch<__bf16, false>(q, s_a, w, s_w, y, M, N, K, st);
+  return dispatch({q, s_a, w, s_w, y, M, N, K, st, false}, type);
 }
 
 }  // namespace prism

@@ -359,7 +359,7 @@ int prism_gemm_fp8_blockscale(const uint8_t* q, const float* s_a, const uint8_t*
   int st = check_gemm(q, s_a, w, s_w, y ? q : nullptr, nullptr, M, N, K, 16, &noop);
   if (st != PRISM_OK || noop) return st;
   if (!aligned(s_w, 4) || !aligned(y, type_size(y_type))) return PRISM_ERR_ALIGNMENT;
-  if (((M + 15) / 16) * ((N + 15) / 16) > INT_MAX) return PRISM_ERR_INVALID_ARG;  // grid size
+  if ((st = prism::check_gemm_fp8_grid(q, w, y_type, (int)M, (int)N, (int)K)) != PRISM_OK) return st;
   if ((st = check_device()) != PRISM_OK) return st;
   return prism::launch_gemm_fp8(q, s_a, w, s_w, y, y_type, (int)M, (int)N, (int)K, static_cast<hipStream_t>(stream));
 }

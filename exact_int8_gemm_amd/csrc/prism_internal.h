@@ -90,6 +90,8 @@ int launch_quantize_tiles_fp8(const void* x, int type, int64_t ld, uint8_t* q, f
                               hipStream_t st);
 int launch_swiglu_quantize_fp8(const void* gate, const void* up, int type, int64_t ld, uint8_t* q, float* scale,
                                int64_t M, int64_t K, hipStream_t st);
+// PRISM_ERR_INVALID_ARG where the launch that launch_gemm_fp8 chooses has too many threads.
+int check_gemm_fp8_grid(const uint8_t* q, const uint8_t* w, int type, int M, int N, int K);
 int launch_gemm_fp8(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int type, int M,
                     int N, int K, hipStream_t st);
 int64_t token_logprobs_bytes(int64_t M, int64_t V, int top);

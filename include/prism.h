@@ -60,7 +60,7 @@ extern "C" {
 
 /* Status codes. */
 #define PRISM_OK 0
-#define PRISM_ERR_INVALID_ARG (-1) /* null required pointer, negative size, N or K = 0 with M > 0, K > PRISM_K_MAX, unknown type, row stride below the row, workspace too small */
+#define PRISM_ERR_INVALID_ARG (-1) /* null required pointer, negative size, N or K = 0 with M > 0, K > PRISM_K_MAX, unknown type, row stride below the row, workspace too small, a size whose launch would have 2^32 threads or more */
 #define PRISM_ERR_ALIGNMENT (-2)   /* misaligned pointer, or K not a multiple of 16 (32 for block-scale and W4A8, 256 for Q4_K) */
 #define PRISM_ERR_UNSUPPORTED (-3) /* the current device is not gfx950, or no device is usable */
 #define PRISM_ERR_LAUNCH (-4)      /* the kernel launch reported an error */

@@ -95,6 +95,14 @@ CASES += [("prism_gemm_fp8_blockscale", a, e) for a, e in [
     (_g(q=None), INVALID), (_g(sa=None), INVALID), (_g(w=None), INVALID), (_g(sw=None), INVALID), (_g(y=None), INVALID),
     (_g(K=72), ALIGN), (_g(q=A + 8), ALIGN), (_g(w=A + 8), ALIGN), (_g(sa=A + 2), ALIGN), (_g(sw=A + 2), ALIGN),
     (_g(y=A + 1), ALIGN), (_g(t=F32, y=A + 2), ALIGN)]]
+# grids of 2^32 threads: 16 columns a workgroup of 256, 64 x 64 and 128 x 128 tiles
+CASES += [("prism_gemm_fp8_blockscale", a, e) for a, e in [
+    (_g(M=1, N=1 << 28, K=16), INVALID), (_g(M=1, N=(1 << 28) - 16, K=16), UNSUP),
+    (_g(M=8, N=1 << 28, K=16, t=F16), INVALID), (_g(M=4, N=(1 << 31) - 1, K=16, t=F32), INVALID),
+    (_g(M=9, N=1 << 30, K=16, t=F32), INVALID), (_g(M=9, N=(1 << 30) - 64, K=16, t=F32), UNSUP),
+    (_g(M=9, N=1 << 30, K=16, t=F16), INVALID), (_g(M=9, N=1 << 30, K=16), UNSUP),
+    (_g(M=9, N=(1 << 31) - 1, K=16), INVALID), (_g(M=(1 << 31) - 1, N=16, K=16), INVALID),
+    (_g(M=(1 << 31) - 128, N=16, K=16), UNSUP), (_g(M=1 << 20, N=1 << 20, K=16), INVALID)]]
 _BIG = 1 << 20   # a vocabulary of several chunks
 CASES += [("prism_token_logprobs", a, e) for a, e in [
     (_l(), UNSUP), (_l(t=BF16, z=A + 2), UNSUP), (_l(tok=None, T=0, lp=None), UNSUP),
