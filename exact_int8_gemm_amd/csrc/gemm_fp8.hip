@@ -28,6 +28,7 @@
 // weight row 4 (l / 16) + r, activation row l % 16.
 #include "fp8_math.h"
 #include "lds_copy.h"
+#include "wave.h"
 
 namespace prism {
 namespace {
@@ -40,12 +41,6 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 
 // Workgroup barrier that the compiler may not move memory accesses across.
 __device__ inline void barrier() { asm volatile("s_barrier" ::: "memory"); }
-
-// Orders a wave's own LDS accesses, which the hardware keeps in order.
-__device__ inline void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
 
 // f rounded to an output.  f is opaque here: the compiler would otherwise make
 // one instruction of the last fma and the rounding to fp16, without the fp32

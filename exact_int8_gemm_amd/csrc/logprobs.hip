@@ -31,6 +31,7 @@
 // 20: 20 and 8 us; 51 MB).
 #include "../../include/prism.h"
 #include "prism_internal.h"
+#include "wave.h"
 
 namespace prism {
 namespace {
@@ -165,12 +166,6 @@ __device__ inline float kth_of_wave(float g, float largest, int top) {
 // Lanes below this one in a mask.
 __device__ inline int lanes_below(uint64_t mask) {
   return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-}
-
-// Orders this wave's LDS accesses: what its lanes wrote before is read after.
-__device__ inline void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
 }
 
 template <int NT>
@@ -338,7 +333,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
     // values; where there are more than kPieces of them, only their number counts.
     auto gather = [&](auto&& wanted) __attribute__((always_inline)) {
       int np = 0;
-      wave_sync();
+      wave_order();
 #pragma unroll
       for (int it = 0; it < kIter; ++it) {
         const bool in = wanted(gm[it]);
@@ -351,7 +346,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
         }
         np += __popcll(who);
       }
-      wave_sync();
+      wave_order();
       return np;
     };
     auto collect_pieces = [&](int np, auto&& wanted) __attribute__((always_inline)) {
@@ -363,20 +358,20 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
     // The lanes with values of at least t whole, one after the other; f returns
     // whether to go on.
     auto visit = [&](auto&& f) __attribute__((always_inline)) {
-      wave_sync();
+      wave_order();
       for (uint64_t left = __ballot(mt >= t); left != 0;) {
         const int slot = lanes_below(left);
         if ((left >> lane & 1) && slot < kHold) {
 #pragma unroll
           for (int it = 0; it < kIter; ++it) *reinterpret_cast<v4i*>(held + slot * kRow + it * 16) = raw[it];
         }
-        wave_sync();
+        wave_order();
         for (int j = 0; j < kHold && left != 0; ++j, left &= left - 1) {
           const int src = __builtin_ctzll(left);
           const float v = to_float(reinterpret_cast<const T*>(held + j * kRow)[lane]);
           if (!f(v, ((lane / kVec) * 64 + src) * kVec + lane % kVec)) return;
         }
-        wave_sync();
+        wave_order();
       }
     };
     auto reaches = [&](float v) { return v >= t; };
@@ -421,7 +416,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
       }
     }
     if (n <= kCand) {
-      wave_sync();
+      wave_order();
       rank_keys<64>(cand, n, top, best);
     } else {
       // Many different values above t (a chunk whose large values share few
@@ -438,7 +433,7 @@ __global__ __launch_bounds__(64 * WAVES) void logprobs_chunk_kernel(
         if (lane == 0) best[r] = last;
       }
     }
-    wave_sync();
+    wave_order();
   }
   if (chunks == 1) {
     write_row<T, 64>(z, V, row, st, best, tokens, ntok, top, lp, lse, ent, top_ids, top_lp);
