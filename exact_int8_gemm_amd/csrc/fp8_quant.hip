@@ -7,11 +7,12 @@
 // All three read each value once with 16-byte loads, keep it in registers
 // between the absmax and the codes, and write each code once: they are bound
 // by HBM.  16 neighbouring lanes hold one 128-block, 8 values each, so the
-// absmax of a block is four cross-lane steps and no LDS.  Against a large
-// copy's rate: 8192 x 5120 bf16 24.9 us (floor 25), tiles of 17400 x 5120 bf16
-// 55 us (53), SwiGLU of 2048 x 17360 bf16 36.8 us (35); 16 x 5120 fp32 2.8 us
-// and SwiGLU of 4 x 9728 3.2 us are the latency of one load, one reduction and
-// one store.
+// absmax of a block is four cross-lane steps and no LDS.  Kernels alone against
+// a large copy's rate: 8192 x 5120 bf16 25.0 us (floor 25), tiles of 17400 x 5120
+// bf16 56.6 us (53), SwiGLU of 2048 x 17360 bf16 37.1 us (35); 16 x 5120 fp32 and
+// SwiGLU of 4 x 9728, 2.8 us each, are the latency of one load, one reduction and
+// one store.  Back to back, with the writes of the call before still under way,
+// the large ones take 28, 55 and 40 us.
 #include "fp8_math.h"
 
 namespace prism {

@@ -26,6 +26,11 @@
 // codes of a block are the two 16-byte chunks l / 16 and l / 16 + 4.  The
 // weights are the instructions' A operand, so result register r of lane l is
 // weight row 4 (l / 16) + r, activation row l % 16.
+//
+// Times in this file are those of calls back to back.  Single ones are with
+// inputs rotated through 0.6 GB or more unless they say otherwise; forms that
+// are compared were timed in one run.  Traced one launch at a time, large products take 5 to 10% longer
+// (8192 x 5120 x 5120: bf16 191 and 203 us, fp32 380 and 404).
 #include "fp8_math.h"
 #include "lds_copy.h"
 #include "wave.h"
@@ -143,9 +148,9 @@ __device__ inline v4f block_sum(const Operand16<true>& a, const Operand16<true>&
 // issued before this one's are used) and leaves the sums in LDS with the
 // blocks' scales s_a s_w; after one barrier, threads fold the round's blocks
 // into their outputs in order.  Rows past RP (4 where M <= 4) are not stored.
-// M = 1, 5120 x 5120, bf16: 7.3 us with weights in the cache behind the L2s, 8.9
+// M = 1, 5120 x 5120, bf16: 7.3 us with weights in the cache behind the L2s, 8.4
 // from HBM (26 MB: 5.2 at a large copy's rate, which 100003 x 2560 at M = 4
-// reaches: 46 to 49 us, 5.4 TB/s).
+// nearly reaches: fp32 53 us, 4.8 TB/s).
 template <typename OUT, bool EXACT, int MT, int RP, int CB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void gemm_fp8_small_kernel(const uint8_t* __restrict__ q,
                                                                     const float* __restrict__ s_a,
@@ -329,8 +334,8 @@ int launch_small_rows(const Call& c) {
 // taken away, the kernels take the same time).
 //
 // What bounds the 256 x 256 form, MI355X, M = N = K = 8192 (480-510 us, 2.2
-// PFLOP/s; 8192 x 5120 x 5120: 181 to 193 us, 2.3 PFLOP/s): the matrix cores are
-// busy 58% of the cycles at a clock that the power limit holds at 1.9 GHz; without
+// PFLOP/s; 8192 x 5120 x 5120: 188 to 193 us, 2.25 PFLOP/s): the matrix cores are
+// busy 58 to 61% of the cycles at a clock that the power limit holds at 1.9 GHz; without
 // the copies it takes 423 us, without the LDS reads 416, without the folds
 // 405, without either barrier 465.  Times of these parts add up rather than
 // hide behind each other, because each costs clock.  Other forms measured and
@@ -341,10 +346,10 @@ int launch_small_rows(const Call& c) {
 // The smaller forms are bound by a stage's chain of copies, barrier, LDS reads
 // and MFMAs, whatever R is (500 x 2560 x 9600, 160 tiles of 64 x 128: 27 to 32
 // us, 36 from HBM; in one run of 32 us, without copies 21, without LDS reads 28,
-// without the barrier 29, without all three 15).  The fp32 form, 128 x 128, is
-// bound by the f16 MFMAs and the conversions, which share a SIMD's issue (8192 x
-// 5120 x 5120: 373 to 385 us, MFMAs 52% busy; 305 at the rate of a large 16-bit
-// library product).  Spread between the MFMAs, the conversions took 4% fewer
+// without the barrier 29, without all three 15).  The form of exact products,
+// 128 x 128, is bound by the f16 MFMAs and the conversions, which share a SIMD's
+// issue (8192 x 5120 x 5120, fp32 y: 370 to 380 us, MFMAs 53% busy; 305 at the
+// rate of a large 16-bit library product).  Spread between the MFMAs, the conversions took 4% fewer
 // cycles and the same time, at a lower clock.
 template <int WN, int TM, int TN, int R>
 constexpr int kTileLds = R * ((32 * TM + 16 * TN * WN) * kBlock + 128 * WN * 4);  // R stages
@@ -719,8 +724,9 @@ int launch_tile(const Call& c, int64_t full) {
 // Number of compute units that the choices below count with (MI355X).
 constexpr int kCus = 256;
 
-// Kernel for (M, N), fitted on MI355X with inputs rotated through 0.6 GB (us
-// below; every choice gives the same bits):
+// Kernel for (M, N), fitted on MI355X with up to eight sets of inputs in turn (us
+// below; small operands then come from the cache behind the L2s, large ones from
+// HBM; every choice gives the same bits):
 //  * small kernel: M <= 8; up to 16 rows where N <= 16384 (17408 x 5120, M =
 //    16: 64 x 64 tiles 20.6 against 24.0), up to 32 rows where N <= 6144 (5120
 //    x 5120, M = 32: 11.9 against 15.0), for an fp32 or f16 y up to 64 rows there
@@ -747,11 +753,14 @@ int launch(const Call& c) {
     return launch_small_rows<OUT, EXACT>(c);
   const int64_t t64 = tiles(64, 64), t128 = tiles(128, 128), rest = t128 % (2 * kCus);
   const float c128 = (float)(t128 / (2 * kCus)) + (rest == 0 ? 0.0f : rest <= kCus ? 0.66f : 1.0f);
-  // Rows that do not all start on a cache line: the short tiles' own form, with
-  // operands from HBM (us: 500 x 2560 x 9680 48.1 -> 37.0, 1000 x 1300 x 5104 20.9
-  // -> 20.0; from the cache behind the L2s 34.2 and 34.5, 20.9 and 20.8).  Short K
-  // does not pay for its longer ring (300 x 1300 x 2064 7.4, 8.2 so), nor does an
-  // exact sum, which is bound elsewhere (128 x 5120 x 5104 21.0 and 22.4).
+  // Rows that do not all start on a cache line: the short tiles' own form, for
+  // operands from HBM, as a model's weights are.  Sums of five shapes each, 34 to
+  // 1000 rows by 640 to 9728 columns, blocks and lines (us): K = 1040 35.8 and 37.7,
+  // 2064 50.5 and 49.8, 4112 78.7 and 75.2, 5104 89.9 and 86.6, 6160 122 and 112,
+  // 9680 191 and 164, 14352 306 and 248; single shapes from -25% to, with few
+  // columns, +12%.  Operands that stay in the cache behind the L2s lose by it: 4112
+  // 57 and 67, 9680 126 and 138, 14352 209 and 211.  An exact sum is bound elsewhere
+  // (fp32 128 x 5120 x 5104 21.0 and 22.4).
   const bool lines = K >= 4096 && (K % kBlock != 0 || reinterpret_cast<uintptr_t>(c.q) % kBlock != 0 ||
                                    reinterpret_cast<uintptr_t>(c.w) % kBlock != 0);
 #define PRISM_FP8_SHORT(WN, OCC, FULL)                                                 \

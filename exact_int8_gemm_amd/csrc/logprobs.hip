@@ -13,8 +13,9 @@
 // wave each, so a row's sums are always added in the same order.  A chunk is
 // read once and stays in registers: maximum, sums, and its `top` largest
 // values; a second kernel joins the chunks of a row.  Waves do not wait for
-// each other.  2048 x 100003 bf16, both kernels: 95 us with top 8, 73 without
-// (410 MB: 81 us at a large copy's rate).  With four waves and five barriers to
+// each other.  2048 x 100003 bf16, both kernels, calls back to back from HBM: 96
+// us with top 8, 75 without (410 MB: 81 us at a large copy's rate; traced one
+// launch at a time 103 and 8.6).  With four waves and five barriers to
 // each 8192 values, which left the vector units idle 40% of the time, it took
 // 150 us.  What bounds it now is issue: per value an exp at a quarter of the
 // rate and six other instructions; held to 96 or fewer registers for more
@@ -28,7 +29,11 @@
 // values tie at t (a chunk masked to one finite value), the larger ones are
 // ranked and the tied ones marked, of which the first are taken; the join then
 // merges the chunks' sorted keys (256 x 100003 f16, all of the lowest value, top
-// 20: 20 and 8 us; 51 MB).
+// 20: 29 us, about what random values take; 51 MB).  The slowest rows are those whose
+// large values, more than are ranked at once, share few lanes: their lanes are
+// visited once for each listed value (256 x 100003 bf16, top 32: random 30 us,
+// ascending 471, large ones in 4 to 31 lanes 431 to 449; fp32 ascending 37, large
+// ones in 4 lanes 411).
 #include "../../include/prism.h"
 #include "prism_internal.h"
 #include "wave.h"
