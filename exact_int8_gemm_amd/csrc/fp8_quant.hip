@@ -107,35 +107,43 @@ __global__ __launch_bounds__(256) void quantize_tiles_kernel(const T* __restrict
     if (k < K && row0 + 16 * i < M) *reinterpret_cast<v2i*>(q + (row0 + 16 * i) * K + k) = codes8(v[i], s);
 }
 
+// Blocks per lane group: two once there are many workgroups per CU, since
+// fewer cache lines are then shared by workgroups of different dies where rows
+// do not start on a line (2048 x 17360 SwiGLU 38.8 -> 36.8 us; 8192 x 5120 26.4
+// -> 24.9; one block is faster below, 2048 x 2560 5.5 against 5.7).
+int blocks_per_group(int64_t M, int64_t K) { return (M + 15) / 16 * ((K + kBlock - 1) / kBlock) >= 4096 ? 2 : 1; }
+
 template <typename T, bool GLU>
 int launch_blocks(const void* x, const void* up, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,
                   hipStream_t st) {
-  const int kb = (int)((K + kBlock - 1) / kBlock);
-  const int64_t rows16 = (M + 15) / 16;
   const T* xp = static_cast<const T*>(x);
   const T* upp = static_cast<const T*>(up);
-  // Two blocks a lane group once there are many workgroups per CU: fewer cache
-  // lines are shared by workgroups of different dies where rows do not start
-  // on a line (2048 x 17360 SwiGLU 38.8 -> 36.8 us; 8192 x 5120 26.4 -> 24.9;
-  // one block is faster below, 2048 x 2560 5.5 against 5.7).
-  if (rows16 * kb >= 4096) {
-    const int cg = (kb + 1) / 2;
-    quantize_blocks_kernel<T, 2, GLU><<<(unsigned)(rows16 * cg), 256, 0, st>>>(xp, upp, ld, q, scale, M, (int)K, cg);
-  } else {
-    quantize_blocks_kernel<T, 1, GLU><<<(unsigned)(rows16 * kb), 256, 0, st>>>(xp, upp, ld, q, scale, M, (int)K, kb);
-  }
+  const unsigned groups = (unsigned)quantize_blocks_groups(M, K);
+  const int cg = (int)(groups / ((M + 15) / 16));
+  if (blocks_per_group(M, K) == 2)
+    quantize_blocks_kernel<T, 2, GLU><<<groups, 256, 0, st>>>(xp, upp, ld, q, scale, M, (int)K, cg);
+  else
+    quantize_blocks_kernel<T, 1, GLU><<<groups, 256, 0, st>>>(xp, upp, ld, q, scale, M, (int)K, cg);
   return launch_status();
 }
 
 template <typename T>
 int launch_tiles(const void* x, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K, hipStream_t st) {
   const int kb = (int)((K + kBlock - 1) / kBlock);
-  const int64_t tr = (M + kBlock - 1) / kBlock;
-  quantize_tiles_kernel<T><<<(unsigned)(tr * kb), 256, 0, st>>>(static_cast<const T*>(x), ld, q, scale, M, (int)K, kb);
+  quantize_tiles_kernel<T><<<(unsigned)quantize_tiles_groups(M, K), 256, 0, st>>>(static_cast<const T*>(x), ld, q, scale, M, (int)K, kb);
   return launch_status();
 }
 
 }  // namespace
+
+int64_t quantize_blocks_groups(int64_t M, int64_t K) {
+  const int64_t kb = (K + kBlock - 1) / kBlock, per = blocks_per_group(M, K);
+  return (M + 15) / 16 * ((kb + per - 1) / per);
+}
+
+int64_t quantize_tiles_groups(int64_t N, int64_t K) {
+  return (N + kBlock - 1) / kBlock * ((K + kBlock - 1) / kBlock);
+}
 
 int launch_quantize_blocks_fp8(const void* x, int type, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,
                                hipStream_t st) {

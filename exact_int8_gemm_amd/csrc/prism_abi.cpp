@@ -75,10 +75,10 @@ constexpr int64_t kMaxGroups256 = UINT32_MAX / 256;
 bool known_type(int t) { return t == PRISM_TYPE_F32 || t == PRISM_TYPE_F16 || t == PRISM_TYPE_BF16; }
 int64_t type_size(int t) { return t == PRISM_TYPE_F32 ? 4 : 2; }
 
-// Checks of the fp8 quantizers (x2: the second input of SwiGLU, else x again).
-// group_rows bounds the grid: one workgroup per group_rows rows and 128 k.
+// Checks of the fp8 quantizers (x2: the second input of SwiGLU, else x again);
+// `groups` gives the workgroups of the launch.
 int check_fp8_quant(const void* x, const void* x2, int type, int64_t ld, const void* q, const void* scale, int64_t M,
-                    int64_t K, int group_rows, bool* noop) {
+                    int64_t K, int64_t (*groups)(int64_t, int64_t), bool* noop) {
   *noop = false;
   if (!known_type(type) || M < 0 || K < 0) return PRISM_ERR_INVALID_ARG;
   if (M == 0) {
@@ -87,7 +87,7 @@ int check_fp8_quant(const void* x, const void* x2, int type, int64_t ld, const v
   }
   if (K == 0 || K > PRISM_K_MAX || M > INT_MAX || ld < K || ld > INT64_MAX / 4 / M) return PRISM_ERR_INVALID_ARG;
   if (!x || !x2 || !q || !scale) return PRISM_ERR_INVALID_ARG;
-  if ((M + group_rows - 1) / group_rows * ((K + 127) / 128) > kMaxGroups256) return PRISM_ERR_INVALID_ARG;  // grid size
+  if (groups(M, K) > kMaxGroups256) return PRISM_ERR_INVALID_ARG;  // grid size
   if (K % 16 != 0 || !aligned(x, 16) || !aligned(x2, 16) || ld * type_size(type) % 16 != 0 || !aligned(q, 16) ||
       !aligned(scale, 4))
     return PRISM_ERR_ALIGNMENT;
@@ -327,7 +327,7 @@ int prism_gemm_w8a8_blockscale(const int8_t* q, const float* s_a, const int8_t* 
 int prism_quantize_blocks_fp8(const void* x, int x_type, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,
                               void* stream) {
   bool noop;
-  int st = check_fp8_quant(x, x, x_type, ld, q, scale, M, K, 16, &noop);
+  int st = check_fp8_quant(x, x, x_type, ld, q, scale, M, K, prism::quantize_blocks_groups, &noop);
   if (st != PRISM_OK || noop) return st;
   if ((st = check_device()) != PRISM_OK) return st;
   return prism::launch_quantize_blocks_fp8(x, x_type, ld, q, scale, M, K, static_cast<hipStream_t>(stream));
@@ -336,7 +336,7 @@ int prism_quantize_blocks_fp8(const void* x, int x_type, int64_t ld, uint8_t* q,
 int prism_quantize_tiles_fp8(const void* x, int x_type, int64_t ld, uint8_t* q, float* scale, int64_t N, int64_t K,
                              void* stream) {
   bool noop;
-  int st = check_fp8_quant(x, x, x_type, ld, q, scale, N, K, 128, &noop);
+  int st = check_fp8_quant(x, x, x_type, ld, q, scale, N, K, prism::quantize_tiles_groups, &noop);
   if (st != PRISM_OK || noop) return st;
   if ((st = check_device()) != PRISM_OK) return st;
   return prism::launch_quantize_tiles_fp8(x, x_type, ld, q, scale, N, K, static_cast<hipStream_t>(stream));
@@ -345,7 +345,7 @@ int prism_quantize_tiles_fp8(const void* x, int x_type, int64_t ld, uint8_t* q, 
 int prism_swiglu_quantize_fp8(const void* gate, const void* up, int x_type, int64_t ld, uint8_t* q, float* scale,
                               int64_t M, int64_t K, void* stream) {
   bool noop;
-  int st = check_fp8_quant(gate, up, x_type, ld, q, scale, M, K, 16, &noop);
+  int st = check_fp8_quant(gate, up, x_type, ld, q, scale, M, K, prism::quantize_blocks_groups, &noop);
   if (st != PRISM_OK || noop) return st;
   if ((st = check_device()) != PRISM_OK) return st;
   return prism::launch_swiglu_quantize_fp8(gate, up, x_type, ld, q, scale, M, K, static_cast<hipStream_t>(stream));

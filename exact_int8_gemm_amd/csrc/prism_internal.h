@@ -84,6 +84,8 @@ int launch_gemm_blockscale(const int8_t* q, const float* s_a, const int8_t* w, c
                            int32_t* partials, int M, int N, int K, hipStream_t st);
 
 // fp8 (e4m3) block-128 layer and the token read-out.  `type` is a PRISM_TYPE_*.
+int64_t quantize_blocks_groups(int64_t M, int64_t K);  // workgroups (of 256 threads), SwiGLU's too
+int64_t quantize_tiles_groups(int64_t N, int64_t K);
 int launch_quantize_blocks_fp8(const void* x, int type, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,
                                hipStream_t st);
 int launch_quantize_tiles_fp8(const void* x, int type, int64_t ld, uint8_t* q, float* scale, int64_t M, int64_t K,

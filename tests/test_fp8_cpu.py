@@ -95,6 +95,15 @@ CASES += [("prism_gemm_fp8_blockscale", a, e) for a, e in [
     (_g(q=None), INVALID), (_g(sa=None), INVALID), (_g(w=None), INVALID), (_g(sw=None), INVALID), (_g(y=None), INVALID),
     (_g(K=72), ALIGN), (_g(q=A + 8), ALIGN), (_g(w=A + 8), ALIGN), (_g(sa=A + 2), ALIGN), (_g(sw=A + 2), ALIGN),
     (_g(y=A + 1), ALIGN), (_g(t=F32, y=A + 2), ALIGN)]]
+# grids of 2^32 threads: 16 rows by two blocks a workgroup of 256 (one where the call is small), tiles
+CASES += [(fn, a, e) for fn, a, e in [
+    ("prism_quantize_blocks_fp8", _b(M=(1 << 28) - 16, K=256, ld=256, t=BF16), UNSUP),
+    ("prism_quantize_blocks_fp8", _b(M=1 << 28, K=256, ld=256, t=BF16), INVALID),
+    ("prism_swiglu_quantize_fp8", _s(M=(1 << 28) - 16, K=256, ld=512, t=BF16), UNSUP),
+    ("prism_swiglu_quantize_fp8", _s(M=1 << 28, K=256, ld=512, t=BF16), INVALID),
+    ("prism_quantize_blocks_fp8", _b(M=(1 << 28) - 16, K=128, ld=128, t=BF16), UNSUP),
+    ("prism_quantize_tiles_fp8", _b(M=(1 << 31) - 128, K=128, ld=128, t=BF16), UNSUP),
+    ("prism_quantize_tiles_fp8", _b(M=(1 << 31) - 127, K=128, ld=128, t=BF16), INVALID)]]
 # grids of 2^32 threads: 16 columns a workgroup of 256, 64 x 64 and 128 x 128 tiles
 CASES += [("prism_gemm_fp8_blockscale", a, e) for a, e in [
     (_g(M=1, N=1 << 28, K=16), INVALID), (_g(M=1, N=(1 << 28) - 16, K=16), UNSUP),
