@@ -575,6 +575,12 @@ __global__ __launch_bounds__(NT) void logprobs_join_kernel(
   write_row<T, NT>(logits + row * ld, V, row, st, best, tokens, ntok, top, lp, lse, ent, top_ids, top_lp);
 }
 
+// Threads of a workgroup.  Few chunks: a wave each, to have them on as many CUs.
+int chunk_threads(int64_t total) { return total <= 1024 ? 64 : 256; }
+// A wave per row while its lanes hold a few keys each (2048 rows of 104 keys:
+// 10.5 us with four waves, 7).
+int join_threads(int64_t chunks, int top) { return chunks <= 64 && chunks * top <= 256 ? 64 : 256; }
+
 template <typename T>
 int launch(const void* logits, int64_t ld, const int64_t* tokens, int64_t ntok, int top, float* lp, float* lse,
            float* ent, int64_t* top_ids, float* top_lp, void* ws, int64_t M, int64_t V, hipStream_t st) {
@@ -583,16 +589,13 @@ int launch(const void* logits, int64_t ld, const int64_t* tokens, int64_t ntok, 
   uint64_t* keys = static_cast<uint64_t*>(ws);  // 8-byte entries first
   Stats* stats = reinterpret_cast<Stats*>(keys + (chunks > 1 ? M * chunks * top : 0));
   const unsigned total = (unsigned)(M * chunks);
-  // Few chunks: a wave per workgroup, to have them on as many CUs.
-  if (total <= 1024)
+  if (chunk_threads(total) == 64)
     logprobs_chunk_kernel<T, 1><<<total, 64, 0, st>>>(z, ld, V, total, chunks, top, stats, keys, tokens, ntok, lp, lse,
                                                       ent, top_ids, top_lp);
   else
     logprobs_chunk_kernel<T, 4><<<(total + 3) / 4, 256, 0, st>>>(z, ld, V, total, chunks, top, stats, keys, tokens, ntok,
                                                                  lp, lse, ent, top_ids, top_lp);
-  // A wave per row while its lanes hold a few keys each (2048 rows of 104 keys:
-  // 10.5 us with four waves, 7).
-  if (chunks > 1 && chunks <= 64 && chunks * top <= 256)
+  if (chunks > 1 && join_threads(chunks, top) == 64)
     logprobs_join_kernel<T, 64><<<(unsigned)M, 64, 0, st>>>(z, ld, V, chunks, top, stats, keys, tokens, ntok, lp, lse, ent,
                                                             top_ids, top_lp);
   else if (chunks > 1)
@@ -609,9 +612,12 @@ int64_t token_logprobs_bytes(int64_t M, int64_t V, int top) {
   return chunks > 1 ? M * chunks * (8 * (int64_t)top + (int64_t)sizeof(Stats)) : 0;
 }
 
-int64_t token_logprobs_groups(int64_t M, int64_t V) {
-  const int64_t chunks = (V + kChunk - 1) / kChunk;
-  return chunks > 1 ? (M * chunks + 3) / 4 > M ? (M * chunks + 3) / 4 : M : (M + 3) / 4;
+int64_t token_logprobs_threads(int64_t M, int64_t V, int top) {
+  const int64_t chunks = (V + kChunk - 1) / kChunk, total = M * chunks;
+  const int waves = chunk_threads(total) / 64;
+  const int64_t first = (total + waves - 1) / waves * (64 * waves);
+  const int64_t second = chunks > 1 ? M * join_threads(chunks, top) : 0;
+  return first > second ? first : second;
 }
 
 int launch_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t ntok, int top,

@@ -383,7 +383,7 @@ int prism_token_logprobs(const void* logits, int type, int64_t ld, const int64_t
     return PRISM_ERR_INVALID_ARG;
   const int64_t need = prism::token_logprobs_bytes(M, V, top);
   if (need > 0 && (!workspace || workspace_bytes < need)) return PRISM_ERR_INVALID_ARG;
-  if (prism::token_logprobs_groups(M, V) > kMaxGroups256) return PRISM_ERR_INVALID_ARG;  // grid size
+  if (prism::token_logprobs_threads(M, V, top) > (int64_t)UINT32_MAX) return PRISM_ERR_INVALID_ARG;  // grid size
   if (!aligned(logits, type_size(type)) || !aligned(tokens, 8) || !aligned(logprobs, 4) || !aligned(lse, 4) ||
       !aligned(entropy, 4) || !aligned(top_ids, 8) || !aligned(top_logprobs, 4) || !aligned(workspace, 8))
     return PRISM_ERR_ALIGNMENT;

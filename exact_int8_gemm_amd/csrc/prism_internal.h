@@ -97,7 +97,7 @@ int check_gemm_fp8_grid(const uint8_t* q, const uint8_t* w, int type, int M, int
 int launch_gemm_fp8(const uint8_t* q, const float* s_a, const uint8_t* w, const float* s_w, void* y, int type, int M,
                     int N, int K, hipStream_t st);
 int64_t token_logprobs_bytes(int64_t M, int64_t V, int top);
-int64_t token_logprobs_groups(int64_t M, int64_t V);  // workgroups (of 256 threads)
+int64_t token_logprobs_threads(int64_t M, int64_t V, int top);  // of its larger launch
 int launch_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t ntok, int top,
                           float* lp, float* lse, float* ent, int64_t* top_ids, float* top_lp, void* ws, int64_t M,
                           int64_t V, hipStream_t st);

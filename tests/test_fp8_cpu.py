@@ -127,6 +127,13 @@ CASES += [("prism_token_logprobs", a, e) for a, e in [
     (_l(V=_BIG, ld=_BIG, ws=A, wb=1 << 30), UNSUP), (_l(V=_BIG, ld=_BIG, ws=A + 4, wb=1 << 30), ALIGN),
     (_l(z=A + 2), ALIGN), (_l(t=F16, z=A + 1), ALIGN), (_l(tok=A + 4), ALIGN), (_l(lp=A + 2), ALIGN),
     (_l(lse=A + 2), ALIGN), (_l(ent=A + 2), ALIGN), (_l(ids=A + 4), ALIGN), (_l(tlp=A + 2), ALIGN)]]
+# grids of 2^32 threads: a wave for each 4096 logits, in fours; a wave or, with many keys, four to join a row's
+CASES += [("prism_token_logprobs", a, e) for a, e in [
+    (_l(M=(1 << 26) - 4, top=0), UNSUP), (_l(M=1 << 26, top=0), INVALID),
+    (_l(M=1 << 24, V=4100, ld=4100, t=F16, ws=A, wb=1 << 40), UNSUP),
+    (_l(M=(1 << 25) - 2, V=4100, ld=4100, t=F16, ws=A, wb=1 << 40), UNSUP),
+    (_l(M=1 << 25, V=4100, ld=4100, t=F16, ws=A, wb=1 << 40), INVALID),
+    (_l(M=1 << 20, V=100003, ld=100003, top=32, ws=A, wb=1 << 40), UNSUP)]]
 WS = "prism_token_logprobs_workspace"
 WS_CASES = [([0, 0, 0], OK), ([4, 100, 20], OK), ([4, _BIG, 0], OK), ([4, _BIG, 32], OK), ([-1, 4, 0], INVALID),
             ([1, -4, 0], INVALID), ([1, 4, 33], INVALID), ([1, 4, -1], INVALID), ([1 << 31, 4, 0], INVALID),
