@@ -25,7 +25,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libprism.so")
 
 SOURCES = ["quantize.hip", "gemm_small.hip", "gemm_tiled.hip", "repack.hip", "fp8_quant.hip", "gemm_fp8.hip",
-           "logprobs.hip", "peaks.hip", "prism_abi.cpp"]
+           "gemm_fp8_grouped.hip", "norm_quant.hip", "experts.hip", "logprobs.hip", "peaks.hip", "prism_abi.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

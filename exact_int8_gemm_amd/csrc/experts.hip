@@ -1,0 +1,476 @@
+// Routing of a mixture-of-experts layer, and the weighted sum behind it: the
+// parts around the grouped products (gemm_fp8_grouped.hip) that make them a layer
+// of the quantized model (StartLux-Prism README, "Why StartLux-Prism": a row's
+// result does not depend on what it is batched with).
+//
+// Routing, per token: the `top` experts of largest key, the lower index first
+// among equal keys, their weights, and a counting sort of all choices by expert
+// that keeps the order of the tokens.  The key is the logit itself, or with a bias
+// the score plus the bias in 64 bits, where two experts that differ at all also
+// differ in the key.  One wave takes one token: lane l holds experts V l ... V l + V - 1,
+// the largest key is a maximum over the lanes, and its holder the lowest lane that
+// has it.
+//
+// The sort works on 32 tokens at a time.  A token chooses an expert once at the
+// most, so an expert's tokens are the bits of one word, set by atomic ors whose
+// order does not matter; their number is its population count and a choice's
+// rank that of the bits below its own.  One workgroup routes `passes` times 32
+// tokens and leaves its counts per expert; a second launch adds up the counts in
+// front of each workgroup's and places the choices.
+#include <type_traits>
+
+#include "../../include/prism.h"
+#include "prism_internal.h"
+
+namespace prism {
+namespace {
+
+constexpr int kTokens = 32;       // of a pass: the bits of a word
+constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / 64;
+constexpr int kMaxChunks = 512;   // workgroups of a call
+
+struct Route {
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int score, renormalize;
+  float scale;
+  int top;
+  int32_t* ids;
+  float* weights;
+  int32_t* offsets;
+  int32_t* rows;
+  int32_t* slots;
+  uint16_t* counts;  // [workgroups][E]
+  int M, E, passes;
+};
+
+template <int CTRL, int ROWS>
+__device__ inline uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false));
+}
+// Over the wave, without LDS: shifts within rows of 16 lanes, then row broadcasts.
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = dpp_max<0x111, 0xf>(v);  // row_shr:1
+  v = dpp_max<0x112, 0xf>(v);
+  v = dpp_max<0x114, 0xf>(v);
+  v = dpp_max<0x118, 0xf>(v);
+  v = dpp_max<0x142, 0xa>(v);  // row_bcast:15
+  v = dpp_max<0x143, 0xc>(v);  // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ inline uint64_t wave_max(uint64_t k) {
+  const uint32_t hi = wave_max((uint32_t)(k >> 32));
+  const uint32_t lo = wave_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return ((uint64_t)hi << 32) | lo;
+}
+__device__ inline double wave_sum(double v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+__device__ inline int wave_inclusive(int v) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(v, off, 64);
+    if ((int)(threadIdx.x & 63) >= off) v += o;
+  }
+  return v;
+}
+
+// Order of the values, above 0; + 0 makes -0 equal to 0.
+__device__ inline uint32_t order_of(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
+  return (b >> 31) ? ~b : (b | 0x80000000u);
+}
+__device__ inline uint64_t order_of(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
+  return (b >> 63) ? ~b : (b | 0x8000000000000000u);
+}
+
+__device__ inline double readlane(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ inline double sigmoid(double z) { return 1.0 / (1.0 + exp(-z)); }
+
+// One token's choice by a wave.  Lane j < top gets choice j (-1: none left) and its weight.
+template <typename T, int V, bool BIAS>
+__device__ inline void choose(const Route& a, int row, int& id, float& weight) {
+  using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
+  const int lane = threadIdx.x & 63;
+  const T* zp = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+  const float kInf = __builtin_inff();
+  float z[V];
+  bool bad = false;
+  float most = -kInf;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = lane * V + v;
+    z[v] = e < a.E ? (float)zp[e] : -kInf;
+    bad = bad || !(z[v] < kInf);  // NaN or +inf
+    most = fmaxf(most, z[v]);
+  }
+  id = -1;
+  weight = 0.0f;
+  if (__any(bad)) {
+    weight = __builtin_nanf("");
+    return;
+  }
+  const bool softmax = a.score == PRISM_SCORE_SOFTMAX;
+  double shift = 0.0, total = 1.0;  // of the softmax
+  double s[V];
+  if (softmax) {
+    const uint32_t m = wave_max(order_of(most));
+    const float f = __builtin_bit_cast(float, (m >> 31) ? (m & 0x7fffffffu) : ~m);
+    if (f > -kInf) shift = (double)f;
+  }
+  if (BIAS || (softmax && !a.renormalize)) {
+    double mine = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s[v] = softmax ? exp((double)z[v] - shift) : sigmoid((double)z[v]);
+      mine += s[v];
+    }
+    if (softmax) total = wave_sum(mine);
+  }
+  Key key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if constexpr (BIAS) {
+      const int e = lane * V + v;
+      const double k = (softmax ? s[v] / total : s[v]) + (e < a.E ? (double)a.bias[e] : 0.0);
+      key[v] = z[v] > -kInf && k > -__builtin_inf() ? order_of(k) : 0;
+    } else {
+      key[v] = z[v] > -kInf ? order_of(z[v]) : 0;
+    }
+  }
+  double score = 0.0;
+  for (int j = 0; j < a.top; ++j) {
+    Key local = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) local = key[v] > local ? key[v] : local;
+    const Key best = wave_max(local);
+    if (best == 0) break;
+    const int holder = (int)__builtin_ctzll(__ballot(local == best));
+    int which = 0;
+    float value = 0.0f;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v)
+      if (key[v] == best) {
+        which = v;
+        value = z[v];
+      }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (lane == holder && v == which) key[v] = 0;
+    const int e = holder * V + __builtin_amdgcn_readlane(which, holder);
+    const float zv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, value), holder));
+    if (lane == j) {
+      id = e;
+      score = (double)zv;
+    }
+  }
+  if (id >= 0) score = softmax ? exp(score - shift) / total : sigmoid(score);
+  if (a.renormalize) {
+    const double sum = wave_sum(score);
+    score = sum > 0.0 ? score / sum : 0.0;
+  }
+  weight = (float)(score * (double)a.scale);
+}
+
+// What the workgroups of both launches hold.
+struct Shared {
+  uint32_t mask[PRISM_EXPERTS_MAX];  // the pass's tokens of each expert
+  int base[PRISM_EXPERTS_MAX];       // each expert's next place
+  int part[2][kThreads];
+  int waves[kWaves];
+  uint16_t id[kTokens * PRISM_TOP_MAX];
+};
+
+// Exclusive sum of v over the threads.
+__device__ inline int block_exclusive(Shared& s, int v) {
+  const int in = wave_inclusive(v), wave = (int)threadIdx.x / 64;
+  if ((threadIdx.x & 63) == 63) s.waves[wave] = in;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < kWaves; ++w)
+    if (w < wave) before += s.waves[w];
+  __syncthreads();
+  return before + in - v;
+}
+
+// The tokens of the pass that starts at `first`, chosen by the waves.
+template <typename T, int V, bool BIAS>
+__device__ inline void route_pass(const Route& a, Shared& s, int first) {
+  const int lane = threadIdx.x & 63;
+  for (int r = (int)threadIdx.x / 64; r < kTokens && first + r < a.M; r += kWaves) {
+    int id;
+    float weight;
+    choose<T, V, BIAS>(a, first + r, id, weight);
+    if (lane < a.top) {
+      const int64_t at = (int64_t)(first + r) * a.top + lane;
+      a.ids[at] = id;
+      a.weights[at] = weight;
+      s.id[r * a.top + lane] = (uint16_t)id;
+      if (id >= 0) atomicOr(&s.mask[id], 1u << r);
+    }
+  }
+}
+
+// Places the choices of the pass: mask, id and base are there.
+__device__ inline void place_pass(const Route& a, Shared& s, int first) {
+  const int count = min(kTokens, a.M - first) * a.top;
+  for (int i = (int)threadIdx.x; i < count; i += kThreads) {
+    const int r = i / a.top;
+    const uint16_t id = s.id[i];
+    int at = -1;
+    if (id != 0xffff) {
+      at = s.base[id] + __popc(s.mask[id] & ((1u << r) - 1));
+      a.rows[at] = first + r;
+    }
+    a.slots[(int64_t)first * a.top + i] = at;
+  }
+}
+
+// Offsets from an expert's count in each thread; base starts at them plus `before`.
+__device__ inline int start(const Route& a, Shared& s, int total, int before, bool write) {
+  const int t = (int)threadIdx.x;
+  const int offset = block_exclusive(s, t < a.E ? total : 0);
+  if (t < a.E) {
+    s.base[t] = offset + before;
+    if (write) a.offsets[t] = offset;
+    if (t == a.E - 1) {
+      s.waves[0] = offset + total;
+      if (write) a.offsets[a.E] = offset + total;
+    }
+  }
+  __syncthreads();
+  return s.waves[0];
+}
+
+// Rows behind the last choice.
+__device__ inline void fill_rest(const Route& a, int used) {
+  const int64_t all = (int64_t)a.M * a.top;
+  for (int64_t i = used + (int64_t)blockIdx.x * kThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kThreads)
+    a.rows[i] = -1;
+}
+
+// ONE: the call has one workgroup and one pass, and needs no second launch.
+template <typename T, int V, bool BIAS, bool ONE>
+__global__ __launch_bounds__(kThreads) void route_kernel(const Route a) {
+  __shared__ Shared s;
+  const int t = (int)threadIdx.x;
+  int count = 0;
+  for (int p = 0; p < a.passes; ++p) {
+    const int first = ((int)blockIdx.x * a.passes + p) * kTokens;
+    s.mask[t] = 0;
+    __syncthreads();
+    if (first < a.M) route_pass<T, V, BIAS>(a, s, first);
+    __syncthreads();
+    count += __popc(s.mask[t]);
+  }
+  if constexpr (ONE) {
+    const int used = start(a, s, count, 0, true);
+    place_pass(a, s, 0);
+    fill_rest(a, used);
+  } else {
+    if (t < a.E) a.counts[(int64_t)blockIdx.x * a.E + t] = (uint16_t)count;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void place_kernel(const Route a) {
+  __shared__ Shared s;
+  const int t = (int)threadIdx.x, chunk = (int)blockIdx.x;
+  // group g of the threads adds up workgroups g, g + groups, ...
+  const int wide = (a.E + 63) / 64 * 64, groups = kThreads / wide;
+  const int g = t / wide, e = t - g * wide;
+  int before = 0, total = 0;
+  if (g < groups && e < a.E) {
+    for (int c = g; c < (int)gridDim.x; c += groups) {
+      const int n = a.counts[(int64_t)c * a.E + e];
+      total += n;
+      if (c < chunk) before += n;
+    }
+  }
+  s.part[0][t] = before;
+  s.part[1][t] = total;
+  __syncthreads();
+  before = total = 0;
+  if (t < a.E) {
+    for (int i = 0; i < groups; ++i) {
+      before += s.part[0][i * wide + t];
+      total += s.part[1][i * wide + t];
+    }
+  }
+  const int used = start(a, s, total, before, chunk == 0);
+  for (int p = 0; p < a.passes; ++p) {
+    const int first = (chunk * a.passes + p) * kTokens;
+    if (first >= a.M) break;
+    s.mask[t] = 0;
+    __syncthreads();
+    const int count = min(kTokens, a.M - first) * a.top;
+    for (int i = t; i < count; i += kThreads) {
+      const int id = a.ids[(int64_t)first * a.top + i];
+      s.id[i] = (uint16_t)id;
+      if (id >= 0) atomicOr(&s.mask[id], 1u << (i / a.top));
+    }
+    __syncthreads();
+    place_pass(a, s, first);
+    __syncthreads();
+    s.base[t] += __popc(s.mask[t]);
+  }
+  fill_rest(a, used);
+}
+
+int passes_of(int64_t M) {
+  const int64_t most = (int64_t)kTokens * kMaxChunks;
+  return M > most ? (int)((M + most - 1) / most) : 1;
+}
+int chunks_of(int64_t M) {
+  const int64_t per = (int64_t)kTokens * passes_of(M);
+  return (int)((M + per - 1) / per);
+}
+
+template <typename T, int V, bool BIAS>
+int launch_experts(const Route& a, hipStream_t st) {
+  const int chunks = chunks_of(a.M);
+  if (chunks == 1 && a.passes == 1) {
+    route_kernel<T, V, BIAS, true><<<1, kThreads, 0, st>>>(a);
+    return launch_status();
+  }
+  route_kernel<T, V, BIAS, false><<<chunks, kThreads, 0, st>>>(a);
+  place_kernel<<<chunks, kThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+template <typename T, bool BIAS>
+int launch_values(const Route& a, hipStream_t st) {
+  if (a.E <= 64) return launch_experts<T, 1, BIAS>(a, st);
+  if (a.E <= 128) return launch_experts<T, 2, BIAS>(a, st);
+  if (a.E <= 256) return launch_experts<T, 4, BIAS>(a, st);
+  if (a.E <= 512) return launch_experts<T, 8, BIAS>(a, st);
+  return launch_experts<T, 16, BIAS>(a, st);
+}
+
+template <typename T>
+int launch_bias(const Route& a, hipStream_t st) {
+  return a.bias ? launch_values<T, true>(a, st) : launch_values<T, false>(a, st);
+}
+
+// ------------------------------------------------------------ weighted sum
+
+// y[m] = add[m] + sum over j ascending of weights[m][j] x[slots[m][j]], in fp32.
+// Bound by reading x: a thread takes eight columns of a row and has up to eight
+// rows of x on their way.
+constexpr int kAhead = 8;
+
+template <typename T>
+__device__ inline void load_part(const T* p, int n, float* v) {
+  typedef T v8 __attribute__((ext_vector_type(8)));
+  if (n >= 8) {
+    v8 t;
+    __builtin_memcpy(&t, p, sizeof(t));  // rows start anywhere
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? (float)p[e] : 0.0f;
+  }
+}
+
+template <typename T, typename OUT>
+__global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ x, const float* __restrict__ weights,
+                                                      const int32_t* __restrict__ slots, const OUT* add, OUT* y,
+                                                      int R, int M, int top, int N, uint32_t per_row) {
+  const uint32_t at = blockIdx.x * 256u + threadIdx.x;
+  const int m = (int)(at / per_row), n = (int)(at % per_row) * 8;
+  if (m >= M) return;
+  float acc[8];
+  if (add) {
+    load_part(add + (int64_t)m * N + n, N - n, acc);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+  }
+  for (int j0 = 0; j0 < top; j0 += kAhead) {
+    float w[kAhead], v[kAhead][8];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const bool in = j0 + j < top;
+      const int64_t i = (int64_t)m * top + (in ? j0 + j : 0);
+      const int slot = in ? slots[i] : -1;
+      w[j] = in ? weights[i] : 0.0f;
+      if ((uint32_t)slot < (uint32_t)R) {
+        load_part(x + (int64_t)slot * N + n, N - n, v[j]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (j0 + j >= top) break;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(w[j], v[j][e], acc[e]);
+    }
+  }
+  OUT* yp = y + (int64_t)m * N + n;
+  if (N - n >= 8) {
+    typedef OUT v8 __attribute__((ext_vector_type(8)));
+    v8 o;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = (OUT)acc[e];
+    __builtin_memcpy(yp, &o, sizeof(o));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < N - n) yp[e] = (OUT)acc[e];
+  }
+}
+
+template <typename T, typename OUT>
+int launch_combine(const void* x, const float* weights, const int32_t* slots, const void* add, void* y, int R, int M,
+                   int top, int N, hipStream_t st) {
+  const uint32_t per_row = (uint32_t)(N + 7) / 8;
+  combine_kernel<T, OUT><<<(unsigned)(combine_threads(M, N) / 256), 256, 0, st>>>(
+      static_cast<const T*>(x), weights, slots, static_cast<const OUT*>(add), static_cast<OUT*>(y), R, M, top, N,
+      per_row);
+  return launch_status();
+}
+
+}  // namespace
+
+int64_t route_experts_bytes(int64_t M, int64_t E) {
+  const int64_t chunks = chunks_of(M);
+  return chunks <= 1 ? 0 : chunks * E * (int64_t)sizeof(uint16_t);
+}
+
+int launch_route_experts(const void* logits, int type, int64_t ld, const float* bias, int score, int renormalize,
+                         float scale, int top, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows,
+                         int32_t* slots, void* workspace, int M, int E, hipStream_t st) {
+  const Route a{logits, ld, bias, score, renormalize, scale, top, ids, weights, offsets, rows, slots,
+                static_cast<uint16_t*>(workspace), M, E, passes_of(M)};
+  if (type == PRISM_TYPE_F32) return launch_bias<float>(a, st);
+  if (type == PRISM_TYPE_F16) return launch_bias<_Float16>(a, st);
+  return launch_bias<__bf16>(a, st);
+}
+
+int64_t combine_threads(int64_t M, int64_t N) { return (M * ((N + 7) / 8) + 255) / 256 * 256; }
+
+int launch_combine_experts(const void* x, int type, const float* weights, const int32_t* slots, const void* add,
+                           void* y, int y_type, int R, int M, int top, int N, hipStream_t st) {
+  if (type == PRISM_TYPE_F32) return launch_combine<float, float>(x, weights, slots, add, y, R, M, top, N, st);
+  if (type == PRISM_TYPE_F16) {
+    if (y_type == type) return launch_combine<_Float16, _Float16>(x, weights, slots, add, y, R, M, top, N, st);
+    return launch_combine<_Float16, float>(x, weights, slots, add, y, R, M, top, N, st);
+  }
+  if (y_type == type) return launch_combine<__bf16, __bf16>(x, weights, slots, add, y, R, M, top, N, st);
+  return launch_combine<__bf16, float>(x, weights, slots, add, y, R, M, top, N, st);
+}
+
+}  // namespace prism

@@ -1,0 +1,212 @@
+// fp8 (e4m3) GEMM grouped by expert, with ragged groups: rows offsets[e] ..
+// offsets[e + 1] - 1 of the output come from expert e's weights.  The arithmetic
+// is that of gemm_fp8.hip on the same instructions, so that a row has the bits that
+// the dense product with its expert's weights gives it.
+//
+// The groups are known on the device only: the grid is the largest number of row
+// tiles that the sizes allow, each workgroup finds its tile from the offsets, and
+// those past the last one leave at once.
+#include "gemm_fp8_kernels.h"
+
+namespace prism {
+namespace {
+
+using namespace fp8;
+
+// Operands of a call.
+struct Grouped {
+  const uint8_t* q;
+  const float* s_a;
+  const int32_t* rows;     // of q, of each row of y; or null: the same one
+  const int32_t* offsets;
+  const uint8_t* w;
+  const float* s_w;
+  void* y;
+  int M, R, E, N, K;       // M: rows of q, R: of y
+};
+
+struct Tile {
+  int expert, first, rows;  // rows first .. first + rows - 1 of y
+};
+
+__device__ inline int wave_inclusive(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
+
+// Row tile `id` in the list of the groups' tiles of BM rows; false past its end.
+// Whatever the offsets hold, the rows found are rows of y.
+template <int BM>
+__device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int R, int id, Tile& t) {
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int lo = e < E ? min(max(offsets[e], 0), R) : 0;
+    const int hi = e < E ? min(max(offsets[e + 1], lo), R) : 0;
+    const int tiles = (hi - lo + BM - 1) / BM;
+    const int upto = wave_inclusive(tiles);
+    const uint64_t reach = __ballot(upto > id);
+    if (reach) {
+      const int at = (int)__builtin_ctzll(reach);
+      const int in = id - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
+      const int begin = __builtin_amdgcn_readlane(lo, at), end = __builtin_amdgcn_readlane(hi, at);
+      t.expert = e0 + at;
+      t.first = begin + in * BM;
+      t.rows = min(BM, end - t.first);
+      return true;
+    }
+    id -= __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// Few rows a group: as the dense product's kernel for few rows, bound by reading
+// the weights once.
+template <typename OUT, bool EXACT, int MT, int CB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void grouped_small_kernel(const Grouped a, int tiles_n) {
+  constexpr int NT = 64 * WAVES;
+  constexpr int kTile = 16 * 16;
+  constexpr int kOut = MT * CB * kTile;
+  constexpr int kPer = (kOut + NT - 1) / NT;
+  __shared__ __attribute__((aligned(16))) float lp[2][WAVES][kOut];
+  __shared__ float ls[2][WAVES][16 * MT];
+  Tile t;
+  if (!find_tile<16 * MT>(a.offsets, a.E, a.R, (int)(blockIdx.x / (unsigned)tiles_n), t)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int r = lane & 15, g = lane >> 4;
+  const int N = a.N, K = a.K;
+  const int n0 = (int)(blockIdx.x % (unsigned)tiles_n) * 16 * CB;
+  const int KB = (K + kBlock - 1) / kBlock, NB = (N + kBlock - 1) / kBlock;
+  const uint8_t* we = a.w + (size_t)t.expert * (size_t)N * (size_t)K;
+  const auto rw = make_rsrc(we + (size_t)n0 * (size_t)K, (int64_t)(N - n0) * K);
+  const float* swp = a.s_w + ((size_t)t.expert * (size_t)NB + (size_t)(n0 / kBlock)) * (size_t)KB;
+
+  // q's row of each of this lane's rows, and of the row whose scale it holds: -1 past the tile or outside q
+  auto source = [&](int i) __attribute__((always_inline)) {
+    if (i >= t.rows) return -1;
+    const int m = a.rows ? a.rows[t.first + i] : t.first + i;
+    return (uint32_t)m < (uint32_t)a.M ? m : -1;
+  };
+  const uint8_t* xp[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = source(16 * i + r);
+    xp[i] = m < 0 ? nullptr : a.q + (size_t)m * (size_t)K;
+  }
+  const int ms = source(lane);
+
+  struct Round {
+    Frag16 x[MT], w[CB];
+    float sa, sw;
+  };
+  auto load = [&](int b0, Round& d) __attribute__((always_inline)) {
+    const int b = b0 + wave;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = b * kBlock + 16 * g + 64 * h;
+      const bool in = k < K;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        d.x[i].c[h] = in && xp[i] ? *reinterpret_cast<const v4i*>(xp[i] + k) : v4i{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+        d.w[j].c[h] =
+            __builtin_amdgcn_raw_buffer_load_b128(rw, in ? (uint32_t)((16 * j + r) * K + k) : kOutOfRange, 0, 0);
+    }
+    const int bb = b < KB ? b : KB - 1;  // blocks past K are not folded
+    d.sa = ms < 0 ? 0.0f : a.s_a[(size_t)bb * (size_t)a.M + ms];
+    d.sw = swp[bb];
+  };
+  auto multiply = [&](int buf, const Round& d) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const Operand16<EXACT> xo(d.x[i]);
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+        *reinterpret_cast<v4f*>(&lp[buf][wave][(i * CB + j) * kTile + (g * 16 + r) * 4]) =
+            block_sum(Operand16<EXACT>(d.w[j]), xo);
+    }
+    if (lane < 16 * MT) ls[buf][wave][lane] = d.sa * d.sw;
+  };
+  float f[kPer];
+#pragma unroll
+  for (int o = 0; o < kPer; ++o) f[o] = 0.0f;
+  auto fold = [&](int buf, int count) __attribute__((always_inline)) {
+#pragma unroll
+    for (int o = 0; o < kPer; ++o) {
+      const int e = (int)threadIdx.x + NT * o;
+      if (e >= kOut) break;
+      const int m = 16 * (e / kTile / CB) + e / 4 % 16;
+      for (int b = 0; b < count; ++b) f[o] = __builtin_fmaf(lp[buf][b][e], ls[buf][b][m], f[o]);
+    }
+  };
+  Round cur, next;
+  load(0, cur);
+  int buf = 0;
+  for (int b0 = 0; b0 < KB; b0 += WAVES) {
+    load(b0 + WAVES, next);
+    multiply(buf, cur);
+    __syncthreads();
+    fold(buf, KB - b0 < WAVES ? KB - b0 : WAVES);
+    cur = next;
+    buf ^= 1;
+  }
+  OUT* y = static_cast<OUT*>(a.y);
+#pragma unroll
+  for (int o = 0; o < kPer; ++o) {
+    const int e = (int)threadIdx.x + NT * o;
+    if (e >= kOut) break;
+    const int i = e / kTile, m = 16 * (i / CB) + e / 4 % 16;
+    const int n = n0 + 16 * (i % CB) + 4 * (e % kTile / 64) + e % 4;
+    if (m < t.rows && n < N) y[(size_t)(t.first + m) * (size_t)N + (size_t)n] = rounded<OUT>(f[o]);
+  }
+}
+
+constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Row tiles of BM rows that the groups can have at the most: each group's last
+// one may be short, and none is empty.
+int64_t most_tiles(int64_t R, int64_t E, int64_t BM) {
+  const int64_t groups = R < E ? R : E;
+  return (R + groups * (BM - 1)) / BM;
+}
+
+template <typename OUT, bool EXACT, int MT, int CB, int WAVES>
+int launch_small(const Grouped& a, hipStream_t st, bool check) {
+  const int64_t tiles_n = ceil_div(a.N, 16 * CB), groups = tiles_n * most_tiles(a.R, a.E, 16 * MT);
+  if (check) return groups * 64 * WAVES <= (int64_t)UINT32_MAX ? PRISM_OK : PRISM_ERR_INVALID_ARG;
+  grouped_small_kernel<OUT, EXACT, MT, CB, WAVES><<<(unsigned)groups, 64 * WAVES, 0, st>>>(a, (int)tiles_n);
+  return launch_status();
+}
+
+template <typename OUT, bool EXACT>
+int launch(const Grouped& a, hipStream_t st, bool check) {
+  return launch_small<OUT, EXACT, 1, 1, 4>(a, st, check);
+}
+
+int dispatch(const Grouped& a, int type, hipStream_t st, bool check) {
+  if (type == PRISM_TYPE_F32) return launch<float, true>(a, st, check);
+  if (type == PRISM_TYPE_F16) return launch<_Float16, true>(a, st, check);
+  return launch<__bf16, false>(a, st, check);
+}
+
+}  // namespace
+
+int check_gemm_fp8_grouped_grid(int type, int M, int R, int E, int N, int K, bool gathered) {
+  const Grouped a{nullptr, nullptr, gathered ? reinterpret_cast<const int32_t*>(4) : nullptr, nullptr, nullptr,
+                  nullptr, nullptr, M, R, E, N, K};
+  return dispatch(a, type, nullptr, true);
+}
+
+int launch_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
+                            const uint8_t* w, const float* s_w, void* y, int type, int M, int R, int E, int N, int K,
+                            hipStream_t st) {
+  return dispatch({q, s_a, rows, offsets, w, s_w, y, M, R, E, N, K}, type, st, false);
+}
+
+}  // namespace prism

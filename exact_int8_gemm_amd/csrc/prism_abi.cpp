@@ -172,7 +172,7 @@ const char* prism_status_string(int status) {
   switch (status) {
     case PRISM_OK: return "ok";
     case PRISM_ERR_INVALID_ARG:
-      return "invalid argument (null pointer, negative or zero size, K above PRISM_K_MAX, unknown type, row stride "
+      return "invalid argument (null pointer, negative or zero size, K above PRISM_K_MAX or another limit, unknown type, row stride "
              "below the row, or workspace too small)";
     case PRISM_ERR_ALIGNMENT: return "misaligned pointer or K not a multiple of the required block";
     case PRISM_ERR_UNSUPPORTED: return "no usable gfx950 (MI355X) device is current";
@@ -391,6 +391,116 @@ int prism_token_logprobs(const void* logits, int type, int64_t ld, const int64_t
   if (dev != PRISM_OK) return dev;
   return prism::launch_token_logprobs(logits, type, ld, tokens, T, top, logprobs, lse, entropy, top_ids, top_logprobs,
                                       workspace, M, V, static_cast<hipStream_t>(stream));
+}
+
+static int norm_call(const void* x, int x_type, int64_t x_ld, const void* residual, int64_t res_ld, void* residual_out,
+                     int64_t out_ld, int res_type, const void* gain, int gain_type, double eps, void* norm, void* q,
+                     bool int8, float* scale, int64_t M, int64_t K, void* stream) {
+  if (!known_type(x_type) || !known_type(gain_type) || M < 0 || K < 0) return PRISM_ERR_INVALID_ARG;
+  if (!(eps >= 0.0) || eps > 1.7e308) return PRISM_ERR_INVALID_ARG;  // NaN, negative, infinite
+  if (residual && res_type != x_type && res_type != PRISM_TYPE_F32) return PRISM_ERR_INVALID_ARG;
+  if (M == 0) return PRISM_OK;
+  if (K == 0 || K > PRISM_NORM_K_MAX || M > INT_MAX || x_ld < K || x_ld > INT64_MAX / 4 / M)
+    return PRISM_ERR_INVALID_ARG;
+  if (!x || !gain || !q || !scale || (residual_out && !residual)) return PRISM_ERR_INVALID_ARG;
+  if (residual && (res_ld < K || res_ld > INT64_MAX / 4 / M)) return PRISM_ERR_INVALID_ARG;
+  if (residual_out && (out_ld < K || out_ld > INT64_MAX / 4 / M || (residual_out == residual && out_ld != res_ld)))
+    return PRISM_ERR_INVALID_ARG;
+  if (prism::norm_threads(M, K) > (int64_t)UINT32_MAX) return PRISM_ERR_INVALID_ARG;  // grid size
+  const int64_t size = type_size(x_type), res_size = type_size(res_type);
+  if (K % 16 != 0 || !aligned(x, 16) || x_ld * size % 16 != 0 || !aligned(gain, 16) || !aligned(norm, 16) ||
+      !aligned(q, 16) || !aligned(scale, 4))
+    return PRISM_ERR_ALIGNMENT;
+  if (residual && (!aligned(residual, 16) || res_ld * res_size % 16 != 0)) return PRISM_ERR_ALIGNMENT;
+  if (residual_out && (!aligned(residual_out, 16) || out_ld * res_size % 16 != 0)) return PRISM_ERR_ALIGNMENT;
+  const int dev = check_device();
+  if (dev != PRISM_OK) return dev;
+  return prism::launch_add_rmsnorm_quantize(x, x_type, x_ld, residual, res_ld, residual_out, out_ld, res_type, gain,
+                                            gain_type, eps, norm, q, int8, scale, M, K,
+                                            static_cast<hipStream_t>(stream));
+}
+
+int prism_add_rmsnorm_quantize_fp8(const void* x, int x_type, int64_t x_ld, const void* residual, int64_t res_ld,
+                                   void* residual_out, int64_t out_ld, int res_type, const void* gain, int gain_type,
+                                   double eps, void* norm, uint8_t* q, float* scale, int64_t M, int64_t K,
+                                   void* stream) {
+  return norm_call(x, x_type, x_ld, residual, res_ld, residual_out, out_ld, res_type, gain, gain_type, eps, norm, q,
+                   false, scale, M, K, stream);
+}
+
+int prism_add_rmsnorm_quantize_rows(const void* x, int x_type, int64_t x_ld, const void* residual, int64_t res_ld,
+                                    void* residual_out, int64_t out_ld, int res_type, const void* gain, int gain_type,
+                                    double eps, void* norm, int8_t* q, float* scale, int64_t M, int64_t K,
+                                    void* stream) {
+  return norm_call(x, x_type, x_ld, residual, res_ld, residual_out, out_ld, res_type, gain, gain_type, eps, norm, q,
+                   true, scale, M, K, stream);
+}
+
+int prism_route_experts_workspace(int64_t M, int64_t E, int64_t* bytes) {
+  if (M < 0 || E < 0 || M > PRISM_ROUTE_M_MAX || E > PRISM_EXPERTS_MAX || !bytes) return PRISM_ERR_INVALID_ARG;
+  *bytes = prism::route_experts_bytes(M, E);
+  return PRISM_OK;
+}
+
+int prism_route_experts(const void* logits, int type, int64_t ld, const float* bias, int score, int renormalize,
+                        float scale, int top, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows,
+                        int32_t* slots, void* workspace, int64_t workspace_bytes, int64_t M, int64_t E, void* stream) {
+  if (!known_type(type) || M < 0 || E < 0 || top < 1 || top > PRISM_TOP_MAX || workspace_bytes < 0 ||
+      (score != PRISM_SCORE_SOFTMAX && score != PRISM_SCORE_SIGMOID) || !(scale - scale == 0.0f))
+    return PRISM_ERR_INVALID_ARG;
+  if (M == 0) return PRISM_OK;
+  if (E == 0 || E > PRISM_EXPERTS_MAX || top > E || M > PRISM_ROUTE_M_MAX || M * top > INT_MAX || ld < E ||
+      ld > INT64_MAX / 4 / M)
+    return PRISM_ERR_INVALID_ARG;
+  if (!logits || !ids || !weights || !offsets || !rows || !slots) return PRISM_ERR_INVALID_ARG;
+  const int64_t need = prism::route_experts_bytes(M, E);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return PRISM_ERR_INVALID_ARG;
+  if (!aligned(logits, type_size(type)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) ||
+      !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(workspace, 8))
+    return PRISM_ERR_ALIGNMENT;
+  const int dev = check_device();
+  if (dev != PRISM_OK) return dev;
+  return prism::launch_route_experts(logits, type, ld, bias, score, renormalize != 0, scale, top, ids, weights,
+                                     offsets, rows, slots, workspace, (int)M, (int)E,
+                                     static_cast<hipStream_t>(stream));
+}
+
+int prism_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
+                           const uint8_t* w, const float* s_w, void* y, int y_type, int64_t M, int64_t R, int64_t E,
+                           int64_t N, int64_t K, void* stream) {
+  if (!known_type(y_type) || M < 0 || R < 0 || E < 0 || N < 0 || K < 0) return PRISM_ERR_INVALID_ARG;
+  if (R == 0) return PRISM_OK;
+  if (M == 0 || M > INT_MAX || R > INT_MAX || E == 0 || E > PRISM_EXPERTS_MAX || N == 0 || N > INT_MAX || K == 0 ||
+      K > PRISM_K_MAX || E * N > INT64_MAX / K)
+    return PRISM_ERR_INVALID_ARG;
+  if (!q || !s_a || !offsets || !w || !s_w || !y) return PRISM_ERR_INVALID_ARG;
+  if (rows ? M * K >= (int64_t)1 << 31 : M != R) return PRISM_ERR_INVALID_ARG;
+  if (K % 16 != 0 || !aligned(q, 16) || !aligned(w, 16) || !aligned(s_a, 4) || !aligned(s_w, 4) ||
+      !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(y, type_size(y_type)))
+    return PRISM_ERR_ALIGNMENT;
+  int st = prism::check_gemm_fp8_grouped_grid(y_type, (int)M, (int)R, (int)E, (int)N, (int)K, rows != nullptr);
+  if (st != PRISM_OK) return st;
+  if ((st = check_device()) != PRISM_OK) return st;
+  return prism::launch_gemm_fp8_grouped(q, s_a, rows, offsets, w, s_w, y, y_type, (int)M, (int)R, (int)E, (int)N,
+                                        (int)K, static_cast<hipStream_t>(stream));
+}
+
+int prism_combine_experts(const void* x, int x_type, const float* weights, const int32_t* slots, const void* add,
+                          void* y, int y_type, int64_t R, int64_t M, int64_t top, int64_t N, void* stream) {
+  if (!known_type(x_type) || (y_type != x_type && y_type != PRISM_TYPE_F32) || R < 0 || M < 0 || N < 0 || top < 1 ||
+      top > PRISM_TOP_MAX)
+    return PRISM_ERR_INVALID_ARG;
+  if (M == 0) return PRISM_OK;
+  if (N == 0 || R > INT_MAX || M > INT_MAX || N > INT_MAX || prism::combine_threads(M, N) > (int64_t)UINT32_MAX)
+    return PRISM_ERR_INVALID_ARG;
+  if ((R > 0 && !x) || !weights || !slots || !y) return PRISM_ERR_INVALID_ARG;
+  if (!aligned(x, type_size(x_type)) || !aligned(weights, 4) || !aligned(slots, 4) || !aligned(add, type_size(y_type)) ||
+      !aligned(y, type_size(y_type)))
+    return PRISM_ERR_ALIGNMENT;
+  const int dev = check_device();
+  if (dev != PRISM_OK) return dev;
+  return prism::launch_combine_experts(x, x_type, weights, slots, add, y, y_type, (int)R, (int)M, (int)top, (int)N,
+                                       static_cast<hipStream_t>(stream));
 }
 
 int prism_peak_mfma(int64_t iters, int waves_per_simd, int seed, uint32_t* out, void* stream) {

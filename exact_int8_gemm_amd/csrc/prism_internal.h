@@ -102,6 +102,26 @@ int launch_token_logprobs(const void* logits, int type, int64_t ld, const int64_
                           float* lp, float* lse, float* ent, int64_t* top_ids, float* top_lp, void* ws, int64_t M,
                           int64_t V, hipStream_t st);
 
+// Mixture-of-experts layer: norm with an 8-bit output, routing, grouped GEMM and
+// weighted sum.
+int64_t norm_threads(int64_t M, int64_t K);
+int launch_add_rmsnorm_quantize(const void* x, int x_type, int64_t x_ld, const void* residual, int64_t res_ld,
+                                void* residual_out, int64_t out_ld, int res_type, const void* gain, int gain_type,
+                                double eps, void* norm, void* q, bool int8, float* scale, int64_t M, int64_t K,
+                                hipStream_t st);
+int64_t route_experts_bytes(int64_t M, int64_t E);
+int launch_route_experts(const void* logits, int type, int64_t ld, const float* bias, int score, int renormalize,
+                         float scale, int top, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows,
+                         int32_t* slots, void* workspace, int M, int E, hipStream_t st);
+// PRISM_ERR_INVALID_ARG where the launch that launch_gemm_fp8_grouped chooses has too many threads.
+int check_gemm_fp8_grouped_grid(int type, int M, int R, int E, int N, int K, bool gathered);
+int launch_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
+                            const uint8_t* w, const float* s_w, void* y, int type, int M, int R, int E, int N, int K,
+                            hipStream_t st);
+int64_t combine_threads(int64_t M, int64_t N);
+int launch_combine_experts(const void* x, int type, const float* weights, const int32_t* slots, const void* add,
+                           void* y, int y_type, int R, int M, int top, int N, hipStream_t st);
+
 // Measurement kernels (peaks.hip).
 int launch_peak_mfma(int64_t iters, int waves_per_simd, int seed, uint32_t* out, hipStream_t st);
 int launch_peak_read(const void* buf, int64_t bytes, uint32_t* parts, int nparts, hipStream_t st);

@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libprism.so")
 
 PRISM_OK = 0
-ABI_VERSION = 15
+ABI_VERSION = 16
 K_MAX = 131040
 
 # Dispatch-table entries of the W8A8 / W4A8 calls (PRISM_VARIANT_* in include/prism.h).
@@ -82,6 +82,18 @@ def _declare(lib):
     lib.prism_token_logprobs_workspace.argtypes = [i64, i64, i32, ctypes.POINTER(i64)]
     lib.prism_token_logprobs.restype = i32
     lib.prism_token_logprobs.argtypes = [p, i32, i64, p, i64, i32, p, p, p, p, p, p, i64, i64, i64, p]
+    for name in ("prism_add_rmsnorm_quantize_fp8", "prism_add_rmsnorm_quantize_rows"):
+        fn = getattr(lib, name)
+        fn.restype = i32
+        fn.argtypes = [p, i32, i64, p, i64, p, i64, i32, p, i32, ctypes.c_double, p, p, p, i64, i64, p]
+    lib.prism_route_experts_workspace.restype = i32
+    lib.prism_route_experts_workspace.argtypes = [i64, i64, ctypes.POINTER(i64)]
+    lib.prism_route_experts.restype = i32
+    lib.prism_route_experts.argtypes = [p, i32, i64, p, i32, i32, ctypes.c_float, i32, p, p, p, p, p, p, i64, i64, i64, p]
+    lib.prism_gemm_fp8_grouped.restype = i32
+    lib.prism_gemm_fp8_grouped.argtypes = [p, p, p, p, p, p, p, i32, i64, i64, i64, i64, i64, p]
+    lib.prism_combine_experts.restype = i32
+    lib.prism_combine_experts.argtypes = [p, i32, p, p, p, p, i32, i64, i64, i64, i64, p]
     lib.prism_peak_mfma.restype = i32
     lib.prism_peak_mfma.argtypes = [i64, i32, i32, p, p]
     lib.prism_peak_read.restype = i32
@@ -499,6 +511,194 @@ def token_logprobs_workspace(M, V, top):
     n = ctypes.c_int64(0)
     _check(lib().prism_token_logprobs_workspace(M, V, top, ctypes.byref(n)))
     return n.value
+
+
+# --------------------------------------------------------- mixture-of-experts layer
+
+NORM_K_MAX = 65536
+EXPERTS_MAX = 1024
+ROUTE_M_MAX = 16777216
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+NormQuantized = collections.namedtuple("NormQuantized", "q scale residual norm")
+Routing = collections.namedtuple("Routing", "ids weights offsets rows slots")
+
+
+def _add_rmsnorm(fn, q_dtype, scale_shape, x, gain, eps, residual, residual_out, norm, q, scale):
+    dev, M, K, ld = _rows(x, "x")
+    if not isinstance(gain, torch.Tensor) or gain.dtype not in TYPES:
+        raise TypeError("gain must be a float32, float16 or bfloat16 tensor")
+    _is(gain, "gain", gain.dtype, (K,), dev)
+    res_ptr = out_ptr = None
+    res_ld = out_ld = 0
+    res_type = x.dtype
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    else:
+        res_dev, rows, cols, res_ld = _rows(residual, "residual")
+        res_type = residual.dtype
+        if res_type is not x.dtype and res_type is not torch.float32:
+            raise TypeError("residual must be float32 or %s like x, got %s" % (x.dtype, res_type))
+        if res_dev != dev or (rows, cols) != (M, K):
+            raise ValueError("residual must have shape %s on %s" % ((M, K), dev))
+        if residual_out is None:
+            residual_out = torch.empty((M, K), dtype=res_type, device=dev)
+            out_ld = K
+        elif residual_out is residual:
+            out_ld = res_ld
+        else:
+            out_dev, rows, cols, out_ld = _rows(residual_out, "residual_out")
+            if residual_out.dtype is not res_type or out_dev != dev or (rows, cols) != (M, K):
+                raise ValueError("residual_out must be %s of shape %s on %s" % (res_type, (M, K), dev))
+        res_ptr, out_ptr = residual.data_ptr(), residual_out.data_ptr()
+    if norm is True:
+        norm = torch.empty((M, K), dtype=x.dtype, device=dev)
+    elif norm is False or norm is None:
+        norm = None
+    else:
+        _is(norm, "norm", x.dtype, (M, K), dev)
+    if q is None:
+        q = torch.empty((M, K), dtype=q_dtype, device=dev)
+    else:
+        _is(q, "q", q_dtype, (M, K), dev)
+    shape = scale_shape(M, K)
+    if scale is None:
+        scale = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _is(scale, "scale", torch.float32, shape, dev)
+    _launch(fn, dev, x.data_ptr(), TYPES[x.dtype], ld, res_ptr, res_ld, out_ptr, out_ld, TYPES[res_type],
+            gain.data_ptr(), TYPES[gain.dtype], eps, None if norm is None else norm.data_ptr(), q.data_ptr(),
+            scale.data_ptr(), M, K)
+    return NormQuantized(q, scale, residual_out, norm)
+
+
+def add_rmsnorm_quantize_fp8(x, gain, eps=1e-6, residual=None, residual_out=None, norm=False, q=None, scale=None):
+    """Root-mean-square norm of x + residual with the fp8 quantizer behind it, in one pass.
+
+    x float32/float16/bfloat16 [M, K] on the GPU (rows may be strided, as residual's), gain [K] of any of these types,
+    residual [M, K] of x's type or float32 -> NormQuantized(q float8_e4m3fn [M, K], scale float32 [ceil(K/128), M],
+    residual, norm).  residual: x + residual in the residual's type, in residual_out (which may be the residual
+    itself) or a new tensor; None without one.  norm: the norm itself in x's type where `norm` is True or a tensor
+    for it, else None."""
+    return _add_rmsnorm(lib().prism_add_rmsnorm_quantize_fp8, FP8, lambda m, k: (_blocks(k), m), x, gain, eps, residual,
+                        residual_out, norm, q, scale)
+
+
+def add_rmsnorm_quantize_rows(x, gain, eps=1e-6, residual=None, residual_out=None, norm=False, q=None, scale=None):
+    """add_rmsnorm_quantize_fp8 with the int8 row quantizer: q int8 [M, K], scale float32 [M]."""
+    return _add_rmsnorm(lib().prism_add_rmsnorm_quantize_rows, torch.int8, lambda m, k: (m,), x, gain, eps, residual,
+                        residual_out, norm, q, scale)
+
+
+def route_experts(logits, top, score="softmax", bias=None, renormalize=True, scale=1.0, workspace=None):
+    """logits float32/float16/bfloat16 [M, E] on the GPU (rows may be strided) -> Routing(ids int32 [M, top],
+    weights float32 [M, top], offsets int32 [E + 1], rows int32 [M * top], slots int32 [M, top]): each token's `top`
+    experts and their weights, and the list of all choices sorted by expert.
+
+    score: "softmax" or "sigmoid"; bias float32 [E]: added to the scores for the choice only; renormalize: a token's
+    weights are divided by their sum; scale: what they are multiplied by then.  workspace: a uint8 tensor of at least
+    route_experts_workspace(M, E) bytes to use instead of a new one."""
+    dev, M, E, ld = _rows(logits, "logits")
+    top = int(top)
+    if score not in SCORES:
+        raise ValueError("score must be one of %s, got %r" % (sorted(SCORES), score))
+    if not 1 <= top <= TOP_MAX:
+        raise ValueError("top must be from 1 to %d, got %d" % (TOP_MAX, top))
+    if bias is not None:
+        _is(bias, "bias", torch.float32, (E,), dev)
+    need = route_experts_workspace(M, E)
+    if workspace is None:
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    else:
+        _is(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    new = torch.empty if M else torch.zeros  # no token: every expert's rows are none
+    r = Routing(torch.empty((M, top), dtype=torch.int32, device=dev),
+                torch.empty((M, top), dtype=torch.float32, device=dev),
+                new((E + 1,), dtype=torch.int32, device=dev),
+                torch.empty((M * top,), dtype=torch.int32, device=dev),
+                torch.empty((M, top), dtype=torch.int32, device=dev))
+    _launch(lib().prism_route_experts, dev, logits.data_ptr(), TYPES[logits.dtype], ld,
+            None if bias is None else bias.data_ptr(), SCORES[score], 1 if renormalize else 0, scale, top,
+            r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
+            None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), M, E)
+    return r
+
+
+@functools.lru_cache(maxsize=256)
+def route_experts_workspace(M, E):
+    """Bytes of scratch memory that route_experts needs for these sizes (0: none)."""
+    n = ctypes.c_int64(0)
+    _check(lib().prism_route_experts_workspace(M, E, ctypes.byref(n)))
+    return n.value
+
+
+def gemm_fp8_grouped(q, s_a, w, s_w, offsets, rows=None, y=None, out_dtype=torch.float32):
+    """gemm_fp8_blockscale with each expert's weights on its own rows.
+
+    q float8_e4m3fn [M, K], s_a f32 [ceil(K/128), M]; w float8_e4m3fn [E, N, K], s_w f32 [E, ceil(N/128), ceil(K/128)];
+    offsets int32 [E + 1]: rows offsets[e] .. offsets[e + 1] - 1 of y are expert e's; rows int32 [R]: the row of q that
+    each row of y is made from (None: its own, R = M) -> y [R, N] of out_dtype (or of y's type, if y is given).  Rows
+    of y outside every group are not written."""
+    dev = _gpu(q, "q")
+    if q.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("q must be 2-D and w 3-D")
+    M, K = q.shape
+    E, N, _ = w.shape
+    kb = _blocks(K)
+    _is(q, "q", FP8, (M, K), dev)
+    _is(s_a, "s_a", torch.float32, (kb, M), dev)
+    _is(w, "w", FP8, (E, N, K), dev)
+    _is(s_w, "s_w", torch.float32, (E, _blocks(N), kb), dev)
+    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    R = M
+    if rows is not None:
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            raise ValueError("rows must be a 1-D tensor")
+        R = rows.shape[0]
+        _is(rows, "rows", torch.int32, (R,), dev)
+    dtype = out_dtype if y is None else getattr(y, "dtype", None)
+    if dtype not in TYPES:
+        raise TypeError("y must be float32, float16 or bfloat16, got %s" % (dtype,))
+    if y is None:
+        y = torch.empty((R, N), dtype=dtype, device=dev)
+    else:
+        _is(y, "y", dtype, (R, N), dev)
+    _launch(lib().prism_gemm_fp8_grouped, dev, q.data_ptr(), s_a.data_ptr(), None if rows is None else rows.data_ptr(),
+            offsets.data_ptr(), w.data_ptr(), s_w.data_ptr(), y.data_ptr(), TYPES[dtype], M, R, E, N, K)
+    return y
+
+
+def combine_experts(x, weights, slots, add=None, y=None, out_dtype=None):
+    """x float32/float16/bfloat16 [R, N] on the GPU, weights float32 [M, top] and slots int32 [M, top] of a Routing ->
+    y [M, N] = add + sum over j of weights[:, j] x[slots[:, j]], of out_dtype (or y's or add's type, if given; else
+    x's): x's type or float32.  A slot outside x counts as zeros; y may be add itself."""
+    dev = _gpu(x, "x")
+    if x.dim() != 2 or not isinstance(slots, torch.Tensor) or slots.dim() != 2:
+        raise ValueError("x and slots must be 2-D")
+    if x.dtype not in TYPES:
+        raise TypeError("x must be float32, float16 or bfloat16, got %s" % (x.dtype,))
+    R, N = x.shape
+    M, top = slots.shape
+    _is(x, "x", x.dtype, (R, N), dev)
+    _is(weights, "weights", torch.float32, (M, top), dev)
+    _is(slots, "slots", torch.int32, (M, top), dev)
+    dtype = x.dtype if out_dtype is None else out_dtype
+    for t in (add, y):
+        if isinstance(t, torch.Tensor) and out_dtype is None:
+            dtype = t.dtype
+    if dtype is not x.dtype and dtype is not torch.float32:
+        raise TypeError("y must be float32 or %s like x, got %s" % (x.dtype, dtype))
+    if add is not None:
+        _is(add, "add", dtype, (M, N), dev)
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+    else:
+        _is(y, "y", dtype, (M, N), dev)
+    _launch(lib().prism_combine_experts, dev, x.data_ptr(), TYPES[x.dtype], weights.data_ptr(), slots.data_ptr(),
+            None if add is None else add.data_ptr(), y.data_ptr(), TYPES[dtype], R, M, top, N)
+    return y
 
 
 # ------------------------------------------------------------ measurement kernels

@@ -14,8 +14,8 @@
  * Conventions shared by every call:
  *   - Every pointer argument is a DEVICE pointer (HBM of the current HIP
  *     device).  The caller allocates and owns all buffers; the library keeps
- *     no pointer after the call returns and allocates nothing (the one call
- *     that needs scratch memory takes it as an argument).
+ *     no pointer after the call returns and allocates nothing (the calls
+ *     that need scratch memory take it as an argument).
  *   - Except where a row stride is an argument, matrices are dense and
  *     row-major with no padding: x, q are [M][K],
  *     w is [N][K], w4 is [N][K/2], d is [N][K/32], y and acc are [M][N],
@@ -44,7 +44,7 @@ extern "C" {
 #endif
 
 /* Bumped on any change of a signature or of the semantics below. */
-#define PRISM_ABI_VERSION 15
+#define PRISM_ABI_VERSION 16
 
 /* Largest accepted K.  For K <= 131040 every exact sum of K products of two
  * int8 values (|q|, |w| <= 128) lies strictly inside the int32 range. */
@@ -58,9 +58,19 @@ extern "C" {
 /* Largest number of top alternatives of prism_token_logprobs. */
 #define PRISM_TOP_MAX 32
 
+/* Largest K of the norms, and largest number of experts and of rows of a
+ * routed batch. */
+#define PRISM_NORM_K_MAX 65536
+#define PRISM_EXPERTS_MAX 1024
+#define PRISM_ROUTE_M_MAX 16777216
+
+/* What a router's weights are made from (prism_route_experts). */
+#define PRISM_SCORE_SOFTMAX 0
+#define PRISM_SCORE_SIGMOID 1
+
 /* Status codes. */
 #define PRISM_OK 0
-#define PRISM_ERR_INVALID_ARG (-1) /* null required pointer, negative size, N or K = 0 with M > 0, K > PRISM_K_MAX, unknown type, row stride below the row, workspace too small, a size whose launch would have 2^32 threads or more */
+#define PRISM_ERR_INVALID_ARG (-1) /* null required pointer, negative size, N or K = 0 with M > 0, K > PRISM_K_MAX or another of the limits, unknown type, row stride below the row, workspace too small, a size whose launch would have 2^32 threads or more */
 #define PRISM_ERR_ALIGNMENT (-2)   /* misaligned pointer, or K not a multiple of 16 (32 for block-scale and W4A8, 256 for Q4_K) */
 #define PRISM_ERR_UNSUPPORTED (-3) /* the current device is not gfx950, or no device is usable */
 #define PRISM_ERR_LAUNCH (-4)      /* the kernel launch reported an error */
@@ -372,6 +382,112 @@ int prism_token_logprobs_workspace(int64_t M, int64_t V, int top, int64_t* bytes
 int prism_token_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t T, int top,
                          float* logprobs, float* lse, float* entropy, int64_t* top_ids, float* top_logprobs,
                          void* workspace, int64_t workspace_bytes, int64_t M, int64_t V, void* stream);
+
+/*
+ * ---- A mixture-of-experts layer on those codes ----
+ *
+ * The layer of a model whose MLP is a set of experts, in the order of its
+ * calls: norm (fp8), the router's product (any GEMM), prism_route_experts,
+ * prism_gemm_fp8_grouped on the rows that the routing lists, prism_swiglu_
+ * quantize_fp8, prism_gemm_fp8_grouped, prism_combine_experts.  The method's
+ * pages name no such model; what they ask of a layer holds for it too: 8-bit
+ * products, and a row's result independent of its batch (StartLux-Prism README,
+ * "Why StartLux-Prism").
+ *
+ * Root-mean-square norm with the residual's addition in front of it and an
+ * 8-bit quantizer behind it:
+ *   h = x + residual, the fp32 sum rounded to res_type (h = x where residual
+ *       is NULL);
+ *   inv = 1 / sqrt(sum_k h^2 / K + eps), in 64 bits and rounded once to fp32;
+ *   y = (h * inv) * gain, each product rounded to fp32;
+ *   q, scale: the codes and scales of y, as prism_quantize_blocks_fp8 or
+ *       prism_quantize_rows writes them for y in fp32.
+ *   x        [M][K] of x_type, rows x_ld elements apart.
+ *   residual [M][K] of res_type, rows res_ld apart, or NULL.  res_type is
+ *            x_type or PRISM_TYPE_F32 (not looked at where residual is NULL).
+ *   residual_out [M][K] of res_type, rows out_ld apart, output: h.  May be
+ *            NULL, or residual itself with out_ld = res_ld; NULL where residual
+ *            is.
+ *   gain     [K] of gain_type.
+ *   norm     [M][K] of x_type, output: y rounded; may be NULL.
+ *   q        [M][K], output; scale [KB][M] (fp8) or [M] (int8), output.
+ *   eps      a host value, finite and >= 0.
+ * K must be a multiple of 16 and at most PRISM_NORM_K_MAX; every row of x,
+ * residual and residual_out, and gain, norm and q, 16-byte aligned.  Outputs
+ * overlap no input but as said.  A NaN in a row makes all its y NaN.  Rows
+ * never influence each other.
+ */
+int prism_add_rmsnorm_quantize_fp8(const void* x, int x_type, int64_t x_ld, const void* residual, int64_t res_ld,
+                                   void* residual_out, int64_t out_ld, int res_type, const void* gain, int gain_type,
+                                   double eps, void* norm, uint8_t* q, float* scale, int64_t M, int64_t K,
+                                   void* stream);
+int prism_add_rmsnorm_quantize_rows(const void* x, int x_type, int64_t x_ld, const void* residual, int64_t res_ld,
+                                    void* residual_out, int64_t out_ld, int res_type, const void* gain, int gain_type,
+                                    double eps, void* norm, int8_t* q, float* scale, int64_t M, int64_t K,
+                                    void* stream);
+
+/*
+ * Routing: each token's experts and their weights, and the rows of each expert.
+ *   logits [M][E] of `type`, rows ld >= E elements apart, aligned to their
+ *          element size only.  An expert closed to a token is -inf.
+ *   bias   [E] fp32, added to the score for the choice only, or NULL.  An expert
+ *          whose bias is -inf or NaN is chosen by no token.
+ *   score  PRISM_SCORE_SOFTMAX: softmax over the E logits; PRISM_SCORE_SIGMOID.
+ *   top    experts of a token, 1 to PRISM_TOP_MAX and at most E.
+ *   ids     [M][top] int32, output: the experts of largest key, largest first,
+ *           the lower index first among equals.  The key is the logit, with a
+ *           bias the score plus the bias, computed in 64 bits.  -1 where no open
+ *           expert is left.
+ *   weights [M][top] fp32, output: the chosen experts' scores, with
+ *           `renormalize` divided by their sum (0 where that is 0), times `scale`;
+ *           0 beside -1.
+ *   offsets [E + 1] int32, output: expert e has the rows offsets[e] ..
+ *           offsets[e + 1] - 1 of a list of all choices, sorted by expert.
+ *   rows    [M * top] int32, output: the token of each row of the list, ascending
+ *           within an expert; -1 behind the list's end, offsets[E].
+ *   slots   [M][top] int32, output: each choice's row in the list, or -1.
+ *   workspace  prism_route_experts_workspace bytes (8-byte aligned; may be NULL
+ *           if that is 0), free again when the stream passes the call.
+ * A token with a NaN or +inf logit: ids and slots -1, weights NaN.  M up to
+ * PRISM_ROUTE_M_MAX, E up to PRISM_EXPERTS_MAX, M * top up to 2^31 - 1.
+ */
+int prism_route_experts_workspace(int64_t M, int64_t E, int64_t* bytes);
+int prism_route_experts(const void* logits, int type, int64_t ld, const float* bias, int score, int renormalize,
+                        float scale, int top, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows,
+                        int32_t* slots, void* workspace, int64_t workspace_bytes, int64_t M, int64_t E, void* stream);
+
+/*
+ * GEMM grouped by expert, the groups ragged and known on the device only.
+ *   q, s_a  [M][K] e4m3 and [KB][M] fp32, as of prism_quantize_blocks_fp8.
+ *   rows    [R] int32 device values: row i of y is made from row rows[i] of q;
+ *           or NULL: from row i, with M = R.  A row outside [0, M) counts as zeros.
+ *   offsets [E + 1] int32 device values, not descending: rows offsets[e] ..
+ *           offsets[e + 1] - 1 of y belong to expert e.
+ *   w, s_w  [E][N][K] e4m3 and [E][NB][KB] fp32: each expert's as of
+ *           prism_quantize_tiles_fp8.
+ *   y       [R][N] of y_type, output, aligned to its element size.  Rows in
+ *           front of offsets[0] and from offsets[E] on are left as they are.
+ * Row by row the bits of prism_gemm_fp8_blockscale with that expert's weights.
+ * Offsets are taken as clamped to 0 .. R; where they descend, what is written
+ * of y is not specified (nothing else is).  E up to PRISM_EXPERTS_MAX; with rows,
+ * M * K below 2^31.
+ */
+int prism_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
+                           const uint8_t* w, const float* s_w, void* y, int y_type, int64_t M, int64_t R, int64_t E,
+                           int64_t N, int64_t K, void* stream);
+
+/*
+ * A token's expert outputs added up with its weights.
+ *   x       [R][N] of x_type, aligned to its element size.
+ *   weights [M][top] fp32, slots [M][top] int32: as of prism_route_experts; a
+ *           slot outside [0, R) counts as a row of zeros.
+ *   add     [M][N] of y_type, or NULL: what the sum starts from.
+ *   y       [M][N] of y_type, output: x_type or PRISM_TYPE_F32; may be add itself.
+ * f = add (or +0); for j ascending f = fmaf(weights[m][j], x[slots[m][j]], f);
+ * y = f rounded.  top from 1 to PRISM_TOP_MAX.
+ */
+int prism_combine_experts(const void* x, int x_type, const float* weights, const int32_t* slots, const void* add,
+                          void* y, int y_type, int64_t R, int64_t M, int64_t top, int64_t N, void* stream);
 
 /*
  * Measurement kernels (not part of the GEMM path): what this GPU reaches on
