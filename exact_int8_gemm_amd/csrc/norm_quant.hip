@@ -7,7 +7,7 @@
 //   inv = 1 / sqrt(sum h^2 / K + eps), rounded once to fp32
 //   y = (h inv) gain, each product rounded to fp32
 // and the codes and scales of y: e4m3 with a scale per 128 values, or int8 with a
-// scale per row.
+// scale per row, whose scale is one product with 1 / 127.
 //
 // The sum of squares is held in 64 bits: each square is exact there, and what
 // the order of the sum changes is 2^-53 of it, below the rounding to fp32 but
@@ -121,7 +121,7 @@ __global__ __launch_bounds__(C < 8 ? 512 : 1024) void norm_kernel(const Norm a) 
     peak = peaks[0];
     for (int w = 1; w < waves; ++w) peak = max(peak, peaks[w]);
     const bool finite = peak < 0x7f800000u;
-    const float s = quant::row_scale(__builtin_bit_cast(float, peak), finite);
+    const float s = finite ? __builtin_bit_cast(float, peak) * (1.0f / 127.0f) : __builtin_nanf("");
     const bool zero = !finite || s == 0.0f;
     const float r = zero ? 0.0f : quant::fast_recip(s);
     if (threadIdx.x == 0) a.scale[row] = s;

@@ -400,8 +400,10 @@ int prism_token_logprobs(const void* logits, int type, int64_t ld, const int64_t
  *       is NULL);
  *   inv = 1 / sqrt(sum_k h^2 / K + eps), in 64 bits and rounded once to fp32;
  *   y = (h * inv) * gain, each product rounded to fp32;
- *   q, scale: the codes and scales of y, as prism_quantize_blocks_fp8 or
- *       prism_quantize_rows writes them for y in fp32.
+ *   q, scale: the codes and scales of y.  fp8: as prism_quantize_blocks_fp8
+ *       writes them for y in fp32.  Rows (int8): scale[m] = max_k |y| * fp32(1 /
+ *       127), one product, so within one step of prism_quantize_rows's quotient;
+ *       codes as there, clamp(rint(y / scale[m]), -127, 127).
  *   x        [M][K] of x_type, rows x_ld elements apart.
  *   residual [M][K] of res_type, rows res_ld apart, or NULL.  res_type is
  *            x_type or PRISM_TYPE_F32 (not looked at where residual is NULL).

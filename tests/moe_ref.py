@@ -18,7 +18,7 @@ def quantize_int8(y):
     """fp32 [M, K] -> (codes int8, scales fp32 [M])."""
     y = np.asarray(y, np.float32)
     with np.errstate(all="ignore"):
-        s = (np.abs(y).max(1) / np.float32(127)).astype(np.float32)
+        s = np.abs(y).max(1) * (np.float32(1) / np.float32(127))
         s[~np.isfinite(y).all(1)] = np.nan
         t = np.where(s[:, None] > 0, (y / s[:, None]).astype(np.float32), np.float32(0))
         return np.clip(np.rint(t), -127, 127).astype(np.int8), s

@@ -206,7 +206,8 @@ def test_reference_norm_by_hand():
 
 def test_reference_int8_by_hand():
     q, s = ref.quantize_int8([[127.0, 1.5, 2.5, -126.5], [0, 0, 0, 0], [np.inf, 1, 2, 3]])
-    assert list(q[0]) == [127, 2, 2, -126] and s[0] == 1      # ties to even
+    one = np.float32(127) * (np.float32(1) / np.float32(127))
+    assert list(q[0]) == [127, 2, 2, -126] and s[0] == one == 1      # ties to even
     assert not q[1].any() and s[1] == 0 and not q[2].any() and np.isnan(s[2])
 
 

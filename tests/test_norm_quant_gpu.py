@@ -196,14 +196,16 @@ def test_inputs_and_outputs_past_32_bit_offsets(to):
 
 
 def test_feeds_the_products_as_the_quantizers_do():
-    """The codes of a norm kept in fp32 are those of the plain quantizers on it, and go into both products."""
+    """The fp8 codes of a norm kept in fp32 are those of the plain quantizer on it, the int8 ones nearly, and go into both products."""
     x, r, g = inputs(11, 40, 640, "f32", "f32")
     a = prism.add_rmsnorm_quantize_fp8(on(x), on(g), EPS, residual=on(r), norm=True)
     b = prism.add_rmsnorm_quantize_rows(on(x), on(g), EPS, residual=on(r))
     q, s = prism.quantize_blocks_fp8(a.norm)
     assert torch.equal(q.view(torch.uint8), a.q.view(torch.uint8)) and torch.equal(s, a.scale)
     qi, si = prism.quantize_rows(a.norm)
-    assert torch.equal(qi, b.q) and torch.equal(si, b.scale)
+    # its row scale is a quotient, one step from the product at the most; codes then differ next to ties only
+    assert ((si / b.scale - 1).abs() <= 2.0 ** -22).all() and (qi.int() - b.q.int()).abs().max() <= 1
+    assert (qi != b.q).float().mean() <= 1e-3
     w = torch.randn((96, 640), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
     y = prism.gemm_fp8_blockscale(a.q, a.scale, *prism.quantize_tiles_fp8(w))
     wi, swi = prism.quantize_rows(w)
