@@ -226,14 +226,14 @@ __global__ __launch_bounds__(128 * WN, OCC) void gemm_fp8_tile_kernel(const uint
   if (b < full) {
     int tm, tn;
     tile_of(xcd_order(b, full), tiles_m, tiles_n, tm, tn);
-    tile_body<OUT, EXACT, WN, TM, TN, R, LINES>(lds, q, s_a, w, s_w, y, M, N, K, tm * 32 * TM, tn * 16 * TN * WN);
+    tile_body<OUT, EXACT, WN, TM, TN, R, LINES>(lds, q, s_a, M, w, s_w, y, M, N, K, tm * 32 * TM, tn * 16 * TN * WN);
   } else if constexpr (TAIL < TM) {
     constexpr int S = TM / TAIL;
     int tm, tn;
     const int id = xcd_order(b - full, (int)gridDim.x - full);
     tile_of(full + id / S, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * 32 * TM + id % S * 32 * TAIL;
-    if (m0 < M) tile_body<OUT, EXACT, WN, TAIL, TN, RT, false>(lds, q, s_a, w, s_w, y, M, N, K, m0, tn * 16 * TN * WN);
+    if (m0 < M) tile_body<OUT, EXACT, WN, TAIL, TN, RT, false>(lds, q, s_a, M, w, s_w, y, M, N, K, m0, tn * 16 * TN * WN);
   }
 }
 

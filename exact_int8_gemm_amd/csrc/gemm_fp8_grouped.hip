@@ -25,10 +25,6 @@ struct Grouped {
   int M, R, E, N, K;       // M: rows of q, R: of y
 };
 
-struct Tile {
-  int expert, first, rows;  // rows first .. first + rows - 1 of y
-};
-
 __device__ inline int wave_inclusive(int v) {
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
   v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
@@ -39,30 +35,52 @@ __device__ inline int wave_inclusive(int v) {
   return v;
 }
 
-// Row tile `id` in the list of the groups' tiles of BM rows; false past its end.
-// Whatever the offsets hold, the rows found are rows of y.
+// An expert's rows of y, and how many tiles of BM rows they make.  Whatever the
+// offsets hold, they are rows of y.
 template <int BM>
-__device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int R, int id, Tile& t) {
+__device__ inline int tiles_of(const Grouped& a, int e, int& lo, int& hi) {
+  lo = e < a.E ? min(max(a.offsets[e], 0), a.R) : 0;
+  hi = e < a.E ? min(max(a.offsets[e + 1], lo), a.R) : 0;
+  return (hi - lo + BM - 1) / BM;
+}
+
+struct Group {
+  int expert, begin, end;  // rows begin .. end - 1 of y
+  int tile, tiles;         // the row tile found, of how many
+};
+
+// The group that has row tile `id` of all groups' tiles of BM rows; false past the last.
+template <int BM>
+__device__ inline bool find_group(const Grouped& a, int id, Group& g) {
   const int lane = threadIdx.x & 63;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    const int lo = e < E ? min(max(offsets[e], 0), R) : 0;
-    const int hi = e < E ? min(max(offsets[e + 1], lo), R) : 0;
-    const int tiles = (hi - lo + BM - 1) / BM;
+  for (int e0 = 0; e0 < a.E; e0 += 64) {
+    int lo, hi;
+    const int tiles = tiles_of<BM>(a, e0 + lane, lo, hi);
     const int upto = wave_inclusive(tiles);
     const uint64_t reach = __ballot(upto > id);
     if (reach) {
       const int at = (int)__builtin_ctzll(reach);
-      const int in = id - (__builtin_amdgcn_readlane(upto, at) - __builtin_amdgcn_readlane(tiles, at));
-      const int begin = __builtin_amdgcn_readlane(lo, at), end = __builtin_amdgcn_readlane(hi, at);
-      t.expert = e0 + at;
-      t.first = begin + in * BM;
-      t.rows = min(BM, end - t.first);
+      g.expert = e0 + at;
+      g.begin = __builtin_amdgcn_readlane(lo, at);
+      g.end = __builtin_amdgcn_readlane(hi, at);
+      g.tiles = __builtin_amdgcn_readlane(tiles, at);
+      g.tile = id - (__builtin_amdgcn_readlane(upto, at) - g.tiles);
       return true;
     }
     id -= __builtin_amdgcn_readlane(upto, 63);
   }
   return false;
+}
+
+// Row tiles of all groups.
+template <int BM>
+__device__ inline int count_tiles(const Grouped& a) {
+  int n = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 64) {
+    int lo, hi;
+    n += __builtin_amdgcn_readlane(wave_inclusive(tiles_of<BM>(a, e0 + (threadIdx.x & 63), lo, hi)), 63);
+  }
+  return n;
 }
 
 // Few rows a group: as the dense product's kernel for few rows, bound by reading
@@ -75,8 +93,9 @@ __global__ __launch_bounds__(64 * WAVES) void grouped_small_kernel(const Grouped
   constexpr int kPer = (kOut + NT - 1) / NT;
   __shared__ __attribute__((aligned(16))) float lp[2][WAVES][kOut];
   __shared__ float ls[2][WAVES][16 * MT];
-  Tile t;
-  if (!find_tile<16 * MT>(a.offsets, a.E, a.R, (int)(blockIdx.x / (unsigned)tiles_n), t)) return;
+  Group t;
+  if (!find_group<16 * MT>(a, (int)(blockIdx.x / (unsigned)tiles_n), t)) return;
+  const int first = t.begin + t.tile * 16 * MT, rows = min(16 * MT, t.end - first);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int r = lane & 15, g = lane >> 4;
   const int N = a.N, K = a.K;
@@ -88,8 +107,8 @@ __global__ __launch_bounds__(64 * WAVES) void grouped_small_kernel(const Grouped
 
   // q's row of each of this lane's rows, and of the row whose scale it holds: -1 past the tile or outside q
   auto source = [&](int i) __attribute__((always_inline)) {
-    if (i >= t.rows) return -1;
-    const int m = a.rows ? a.rows[t.first + i] : t.first + i;
+    if (i >= rows) return -1;
+    const int m = a.rows ? a.rows[first + i] : first + i;
     return (uint32_t)m < (uint32_t)a.M ? m : -1;
   };
   const uint8_t* xp[MT];
@@ -163,7 +182,7 @@ __global__ __launch_bounds__(64 * WAVES) void grouped_small_kernel(const Grouped
     if (e >= kOut) break;
     const int i = e / kTile, m = 16 * (i / CB) + e / 4 % 16;
     const int n = n0 + 16 * (i % CB) + 4 * (e % kTile / 64) + e % 4;
-    if (m < t.rows && n < N) y[(size_t)(t.first + m) * (size_t)N + (size_t)n] = rounded<OUT>(f[o]);
+    if (m < rows && n < N) y[(size_t)(first + m) * (size_t)N + (size_t)n] = rounded<OUT>(f[o]);
   }
 }
 
@@ -176,17 +195,65 @@ int64_t most_tiles(int64_t R, int64_t E, int64_t BM) {
   return (R + groups * (BM - 1)) / BM;
 }
 
+int check_grid(int64_t groups, int threads) {
+  return groups * threads <= (int64_t)UINT32_MAX ? PRISM_OK : PRISM_ERR_INVALID_ARG;
+}
+
 template <typename OUT, bool EXACT, int MT, int CB, int WAVES>
 int launch_small(const Grouped& a, hipStream_t st, bool check) {
   const int64_t tiles_n = ceil_div(a.N, 16 * CB), groups = tiles_n * most_tiles(a.R, a.E, 16 * MT);
-  if (check) return groups * 64 * WAVES <= (int64_t)UINT32_MAX ? PRISM_OK : PRISM_ERR_INVALID_ARG;
+  if (check) return check_grid(groups, 64 * WAVES);
   grouped_small_kernel<OUT, EXACT, MT, CB, WAVES><<<(unsigned)groups, 64 * WAVES, 0, st>>>(a, (int)tiles_n);
+  return launch_status();
+}
+
+// Many rows a group: the dense product's LDS tiles, 32 TM rows by 16 TN WN columns,
+// ordered expert by expert; a group's last tile is one of 32 TAIL rows where that is
+// enough.
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int OCC, bool GATHER>
+__global__ __launch_bounds__(128 * WN, OCC) void grouped_tile_kernel(const Grouped a, int tiles_n) {
+  constexpr int kLds = kTileLds<WN, TM, TN, R>;
+  static_assert(TAIL <= TM && kLds <= 160 * 1024 / OCC, "LDS");
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kLds];
+  const int total = count_tiles<32 * TM>(a) * tiles_n;
+  if ((int)blockIdx.x >= total) return;
+  const int id = xcd_order((int)blockIdx.x, total);
+  Group t;
+  if (!find_group<32 * TM>(a, id / tiles_n, t)) return;
+  int tm, tn;
+  tile_of(t.tile * tiles_n + id % tiles_n, t.tiles, tiles_n, tm, tn);
+  const int N = a.N, K = a.K;
+  const int m0 = t.begin + tm * 32 * TM, n0 = tn * 16 * TN * WN;
+  const uint8_t* w = a.w + (size_t)t.expert * (size_t)N * (size_t)K;
+  const float* s_w = a.s_w + (size_t)t.expert * (size_t)ceil_div(N, kBlock) * (size_t)ceil_div(K, kBlock);
+  if (TAIL == TM || t.end - m0 > 32 * TAIL)
+    tile_body<OUT, EXACT, WN, TM, TN, R, false, GATHER>(lds, a.q, a.s_a, a.M, w, s_w, static_cast<OUT*>(a.y), t.end, N,
+                                                        K, m0, n0, {a.rows, a.M});
+  else if constexpr (TAIL < TM)
+    tile_body<OUT, EXACT, WN, TAIL, TN, R, false, GATHER>(lds, a.q, a.s_a, a.M, w, s_w, static_cast<OUT*>(a.y), t.end,
+                                                          N, K, m0, n0, {a.rows, a.M});
+}
+
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, int TAIL, int OCC>
+int launch_tile(const Grouped& a, hipStream_t st, bool check) {
+  const int64_t tiles_n = ceil_div(a.N, 16 * TN * WN), groups = tiles_n * most_tiles(a.R, a.E, 32 * TM);
+  if (check) return check_grid(groups, 128 * WN);
+  if (a.rows)
+    grouped_tile_kernel<OUT, EXACT, WN, TM, TN, R, TAIL, OCC, true><<<(unsigned)groups, 128 * WN, 0, st>>>(a, (int)tiles_n);
+  else
+    grouped_tile_kernel<OUT, EXACT, WN, TM, TN, R, TAIL, OCC, false><<<(unsigned)groups, 128 * WN, 0, st>>>(a, (int)tiles_n);
   return launch_status();
 }
 
 template <typename OUT, bool EXACT>
 int launch(const Grouped& a, hipStream_t st, bool check) {
-  return launch_small<OUT, EXACT, 1, 1, 4>(a, st, check);
+  const int64_t mean = a.R / (a.R < a.E ? a.R : a.E);
+  if (mean <= 16) return launch_small<OUT, EXACT, 1, 1, 4>(a, st, check);
+  if (mean <= 64) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
+  if constexpr (!EXACT) {
+    if (mean >= 192) return launch_tile<OUT, EXACT, 4, 8, 4, 2, 4, 1>(a, st, check);
+  }
+  return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
 }
 
 int dispatch(const Grouped& a, int type, hipStream_t st, bool check) {

@@ -163,13 +163,22 @@ __device__ inline uint32_t line_start(const uint8_t* base, int row, int K) {
   return (uint32_t)(reinterpret_cast<uintptr_t>(base) + (uint64_t)row * (uint64_t)K) % kBlock;
 }
 
-// The tile of BM rows from m0 and BN columns from n0.
-template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, bool LINES>
+// Row numbers of the activations of a tile's rows (GATHER): the row of q, which has
+// `count` of them, of each row of y; one outside counts as zeros.
+struct Gather {
+  const int32_t* rows;
+  int count;
+};
+
+// The tile of BM rows from m0, up to row M, and BN columns from n0.  A block's row
+// scales are `pitch` after the block's before.
+template <typename OUT, bool EXACT, int WN, int TM, int TN, int R, bool LINES, bool GATHER = false>
 __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, const uint8_t* __restrict__ q,
-                                                                const float* __restrict__ s_a,
+                                                                const float* __restrict__ s_a, int pitch,
                                                                 const uint8_t* __restrict__ w,
                                                                 const float* __restrict__ s_w, OUT* __restrict__ y,
-                                                                int M, int N, int K, int m0, int n0) {
+                                                                int M, int N, int K, int m0, int n0,
+                                                                const Gather gather = {}) {
   constexpr int NW = 2 * WN;
   constexpr int BM = 32 * TM, BN = 16 * TN * WN;
   static_assert((TN == 2 || TN == 4) && BN % (8 * NW) == 0, "column tiles");
@@ -200,7 +209,8 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   // columns of a 256-byte window (two rows).
   auto swz_a = [](int row) { return (row >> 1) & 7; };
   auto swz_b = [](int row) { return ((row >> 1) & 1) | (((row >> (TN == 4 ? 4 : 3)) & 3) << 1); };
-  const v4i ra = tiled::dma::rsrc_words(q + (size_t)m0 * (size_t)K, (int64_t)min(M - m0, BM) * K);
+  const v4i ra = GATHER ? tiled::dma::rsrc_words(q, (int64_t)gather.count * K)
+                        : tiled::dma::rsrc_words(q + (size_t)m0 * (size_t)K, (int64_t)min(M - m0, BM) * K);
   const v4i rb = tiled::dma::rsrc_words(w + (size_t)n0 * (size_t)K, (int64_t)(N - n0) * K);
   const uint32_t lx0 = tiled::dma::lds_addr(lx), lw0 = tiled::dma::lds_addr(lw);
   const uint32_t lsa0 = tiled::dma::lds_addr(reinterpret_cast<const int8_t*>(lsa));
@@ -234,12 +244,31 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   // the loop by the short tiles (500 x 2560 x 9600 bf16 29.6 -> 27.2 us, 128 x 5120
   // x 5120 14.7 -> 13.8).
   auto each_time = [](uint32_t v) __attribute__((always_inline)) { return TM > 2 ? fresh(v) : v; };
+  // GATHER: this lane's offset in q of each of its activation copies' rows, and that
+  // of the row whose scale it copies; both past the end where there is no such row.
+  constexpr int kCopies = V * TM / 2;
+  uint32_t from[GATHER ? kCopies : 1], scale_from = 0;
+  static_assert(!GATHER || !LINES, "rows that start anywhere are not gathered");
+  if constexpr (GATHER) {
+    auto source_row = [&](int row) __attribute__((always_inline)) {
+      const int m = m0 + row < M ? gather.rows[m0 + row] : -1;
+      return (uint32_t)m < (uint32_t)gather.count ? (uint32_t)m : kOutOfRange;
+    };
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) {
+      const uint32_t m = source_row(arow + 16 * TM * (c % V) + 32 * (c / V) + (lane >> 3));
+      from[c] = m == kOutOfRange ? kOutOfRange : m * (uint32_t)K + ca;
+    }
+    const int row = wave * 64 + lane;
+    const uint32_t m = row < BM ? source_row(row) : kOutOfRange;
+    scale_from = m == kOutOfRange ? kOutOfRange : m * 4u;
+  }
   // Rows past M or N lie past their buffer's end and chunks past K are sent
   // there: both read zeros.
   auto copy_x = [&](int c, int b, int buf) __attribute__((always_inline)) {  // c = V pair + v
     const uint32_t ck = (uint32_t)b * kBlock;
     const int row = arow + 16 * TM * (c % V) + 32 * (c / V);
-    const uint32_t in = each_time(xoff) + ((uint32_t)(row * K) + ck);
+    const uint32_t in = GATHER ? from[GATHER ? c : 0] + ck : each_time(xoff) + ((uint32_t)(row * K) + ck);
     const uint32_t o = ca + ck < (uint32_t)K ? in : kOutOfRange;
     tiled::dma::copy_to_lds(ra, lx0 + (uint32_t)(buf * kXBuf + row * kBlock), o);
   };
@@ -253,9 +282,12 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
   };
   auto copy_s = [&](int b, int buf) __attribute__((always_inline)) {
     const int bb = b < KB ? b : KB - 1;
-    const v4i rs = tiled::dma::rsrc_words(s_a + (size_t)bb * (size_t)M + (size_t)m0,
-                                          b < KB ? (int64_t)min(M - m0, BM) * 4 : 0);
-    tiled::dma::copy4_to_lds(rs, lsa0 + (uint32_t)((buf * kScales + wave * 64) * 4), (uint32_t)(wave * 64 + lane) * 4u);
+    const v4i rs = GATHER ? tiled::dma::rsrc_words(s_a + (size_t)bb * (size_t)pitch,
+                                                   b < KB ? (int64_t)gather.count * 4 : 0)
+                          : tiled::dma::rsrc_words(s_a + (size_t)bb * (size_t)pitch + (size_t)m0,
+                                                   b < KB ? (int64_t)min(M - m0, BM) * 4 : 0);
+    tiled::dma::copy4_to_lds(rs, lsa0 + (uint32_t)((buf * kScales + wave * 64) * 4),
+                             GATHER ? scale_from : (uint32_t)(wave * 64 + lane) * 4u);
   };
   auto copy_behind_q = [&](int c, int b, int buf) __attribute__((always_inline)) {
     if (c < kB) copy_w(c, b, buf);
