@@ -359,7 +359,7 @@ def _blocks(n):
 
 def _launch(fn, dev, *args):
     """fn(*args, the current stream of dev) with dev the current device; raises on a status."""
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         # the raw handle, without a Stream object around it (2 us of a decode call's 8)
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
@@ -524,52 +524,63 @@ NormQuantized = collections.namedtuple("NormQuantized", "q scale residual norm")
 Routing = collections.namedtuple("Routing", "ids weights offsets rows slots")
 
 
-def _add_rmsnorm(fn, q_dtype, scale_shape, x, gain, eps, residual, residual_out, norm, q, scale):
-    dev, M, K, ld = _rows(x, "x")
+def _dense_or_rows(x, name):
+    """_rows, at once where x is contiguous (the checks are a third of a decode call)."""
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.ndim == 2 and x.dtype in TYPES and x.is_contiguous():
+        rows, cols = x.shape
+        return x.device, rows, cols, cols
+    return _rows(x, name)
+
+
+def _add_rmsnorm(fn, int8, x, gain, eps, residual, residual_out, norm, q, scale):
+    dev, M, K, ld = _dense_or_rows(x, "x")
+    dtype = x.dtype
     if not isinstance(gain, torch.Tensor) or gain.dtype not in TYPES:
         raise TypeError("gain must be a float32, float16 or bfloat16 tensor")
     _is(gain, "gain", gain.dtype, (K,), dev)
-    res_ptr = out_ptr = None
+    res_ptr = out_ptr = norm_ptr = None
     res_ld = out_ld = 0
-    res_type = x.dtype
+    res_type = dtype
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
     else:
-        res_dev, rows, cols, res_ld = _rows(residual, "residual")
+        res_dev, rows, cols, res_ld = _dense_or_rows(residual, "residual")
         res_type = residual.dtype
-        if res_type is not x.dtype and res_type is not torch.float32:
-            raise TypeError("residual must be float32 or %s like x, got %s" % (x.dtype, res_type))
-        if res_dev != dev or (rows, cols) != (M, K):
+        if res_type is not dtype and res_type is not torch.float32:
+            raise TypeError("residual must be float32 or %s like x, got %s" % (dtype, res_type))
+        if rows != M or cols != K or res_dev != dev:
             raise ValueError("residual must have shape %s on %s" % ((M, K), dev))
         if residual_out is None:
-            residual_out = torch.empty((M, K), dtype=res_type, device=dev)
+            residual_out = torch.empty(M, K, dtype=res_type, device=dev)
             out_ld = K
         elif residual_out is residual:
             out_ld = res_ld
         else:
-            out_dev, rows, cols, out_ld = _rows(residual_out, "residual_out")
-            if residual_out.dtype is not res_type or out_dev != dev or (rows, cols) != (M, K):
+            out_dev, rows, cols, out_ld = _dense_or_rows(residual_out, "residual_out")
+            if residual_out.dtype is not res_type or rows != M or cols != K or out_dev != dev:
                 raise ValueError("residual_out must be %s of shape %s on %s" % (res_type, (M, K), dev))
         res_ptr, out_ptr = residual.data_ptr(), residual_out.data_ptr()
-    if norm is True:
-        norm = torch.empty((M, K), dtype=x.dtype, device=dev)
-    elif norm is False or norm is None:
+    if norm is False or norm is None:
         norm = None
     else:
-        _is(norm, "norm", x.dtype, (M, K), dev)
+        if norm is True:
+            norm = torch.empty(M, K, dtype=dtype, device=dev)
+        else:
+            _is(norm, "norm", dtype, (M, K), dev)
+        norm_ptr = norm.data_ptr()
+    q_dtype = torch.int8 if int8 else FP8
     if q is None:
-        q = torch.empty((M, K), dtype=q_dtype, device=dev)
+        q = torch.empty(M, K, dtype=q_dtype, device=dev)
     else:
         _is(q, "q", q_dtype, (M, K), dev)
-    shape = scale_shape(M, K)
+    shape = (M,) if int8 else (_blocks(K), M)
     if scale is None:
-        scale = torch.empty(shape, dtype=torch.float32, device=dev)
+        scale = torch.empty(*shape, dtype=torch.float32, device=dev)
     else:
         _is(scale, "scale", torch.float32, shape, dev)
-    _launch(fn, dev, x.data_ptr(), TYPES[x.dtype], ld, res_ptr, res_ld, out_ptr, out_ld, TYPES[res_type],
-            gain.data_ptr(), TYPES[gain.dtype], eps, None if norm is None else norm.data_ptr(), q.data_ptr(),
-            scale.data_ptr(), M, K)
+    _launch(fn, dev, x.data_ptr(), TYPES[dtype], ld, res_ptr, res_ld, out_ptr, out_ld, TYPES[res_type],
+            gain.data_ptr(), TYPES[gain.dtype], eps, norm_ptr, q.data_ptr(), scale.data_ptr(), M, K)
     return NormQuantized(q, scale, residual_out, norm)
 
 
@@ -581,14 +592,13 @@ def add_rmsnorm_quantize_fp8(x, gain, eps=1e-6, residual=None, residual_out=None
     residual, norm).  residual: x + residual in the residual's type, in residual_out (which may be the residual
     itself) or a new tensor; None without one.  norm: the norm itself in x's type where `norm` is True or a tensor
     for it, else None."""
-    return _add_rmsnorm(lib().prism_add_rmsnorm_quantize_fp8, FP8, lambda m, k: (_blocks(k), m), x, gain, eps, residual,
-                        residual_out, norm, q, scale)
+    return _add_rmsnorm(lib().prism_add_rmsnorm_quantize_fp8, False, x, gain, eps, residual, residual_out, norm, q,
+                        scale)
 
 
 def add_rmsnorm_quantize_rows(x, gain, eps=1e-6, residual=None, residual_out=None, norm=False, q=None, scale=None):
     """add_rmsnorm_quantize_fp8 with the int8 row quantizer: q int8 [M, K], scale float32 [M]."""
-    return _add_rmsnorm(lib().prism_add_rmsnorm_quantize_rows, torch.int8, lambda m, k: (m,), x, gain, eps, residual,
-                        residual_out, norm, q, scale)
+    return _add_rmsnorm(lib().prism_add_rmsnorm_quantize_rows, True, x, gain, eps, residual, residual_out, norm, q, scale)
 
 
 def route_experts(logits, top, score="softmax", bias=None, renormalize=True, scale=1.0, workspace=None):
@@ -599,7 +609,7 @@ def route_experts(logits, top, score="softmax", bias=None, renormalize=True, sca
     score: "softmax" or "sigmoid"; bias float32 [E]: added to the scores for the choice only; renormalize: a token's
     weights are divided by their sum; scale: what they are multiplied by then.  workspace: a uint8 tensor of at least
     route_experts_workspace(M, E) bytes to use instead of a new one."""
-    dev, M, E, ld = _rows(logits, "logits")
+    dev, M, E, ld = _dense_or_rows(logits, "logits")
     top = int(top)
     if score not in SCORES:
         raise ValueError("score must be one of %s, got %r" % (sorted(SCORES), score))
@@ -613,15 +623,13 @@ def route_experts(logits, top, score="softmax", bias=None, renormalize=True, sca
             workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     else:
         _is(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    ids = torch.empty(M, top, dtype=torch.int32, device=dev)
     new = torch.empty if M else torch.zeros  # no token: every expert's rows are none
-    r = Routing(torch.empty((M, top), dtype=torch.int32, device=dev),
-                torch.empty((M, top), dtype=torch.float32, device=dev),
-                new((E + 1,), dtype=torch.int32, device=dev),
-                torch.empty((M * top,), dtype=torch.int32, device=dev),
-                torch.empty((M, top), dtype=torch.int32, device=dev))
+    r = Routing(ids, torch.empty_like(ids, dtype=torch.float32), new(E + 1, dtype=torch.int32, device=dev),
+                torch.empty(M * top, dtype=torch.int32, device=dev), torch.empty_like(ids))
     _launch(lib().prism_route_experts, dev, logits.data_ptr(), TYPES[logits.dtype], ld,
             None if bias is None else bias.data_ptr(), SCORES[score], 1 if renormalize else 0, scale, top,
-            r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
+            ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(), r.rows.data_ptr(), r.slots.data_ptr(),
             None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), M, E)
     return r
 
@@ -662,7 +670,7 @@ def gemm_fp8_grouped(q, s_a, w, s_w, offsets, rows=None, y=None, out_dtype=torch
     if dtype not in TYPES:
         raise TypeError("y must be float32, float16 or bfloat16, got %s" % (dtype,))
     if y is None:
-        y = torch.empty((R, N), dtype=dtype, device=dev)
+        y = torch.empty(R, N, dtype=dtype, device=dev)
     else:
         _is(y, "y", dtype, (R, N), dev)
     _launch(lib().prism_gemm_fp8_grouped, dev, q.data_ptr(), s_a.data_ptr(), None if rows is None else rows.data_ptr(),
@@ -684,16 +692,15 @@ def combine_experts(x, weights, slots, add=None, y=None, out_dtype=None):
     _is(x, "x", x.dtype, (R, N), dev)
     _is(weights, "weights", torch.float32, (M, top), dev)
     _is(slots, "slots", torch.int32, (M, top), dev)
-    dtype = x.dtype if out_dtype is None else out_dtype
-    for t in (add, y):
-        if isinstance(t, torch.Tensor) and out_dtype is None:
-            dtype = t.dtype
+    dtype = out_dtype
+    if dtype is None:
+        dtype = getattr(add if y is None else y, "dtype", x.dtype)
     if dtype is not x.dtype and dtype is not torch.float32:
         raise TypeError("y must be float32 or %s like x, got %s" % (x.dtype, dtype))
     if add is not None:
         _is(add, "add", dtype, (M, N), dev)
     if y is None:
-        y = torch.empty((M, N), dtype=dtype, device=dev)
+        y = torch.empty(M, N, dtype=dtype, device=dev)
     else:
         _is(y, "y", dtype, (M, N), dev)
     _launch(lib().prism_combine_experts, dev, x.data_ptr(), TYPES[x.dtype], weights.data_ptr(), slots.data_ptr(),
