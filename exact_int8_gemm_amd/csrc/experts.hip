@@ -21,6 +21,7 @@
 
 #include "../../include/prism.h"
 #include "prism_internal.h"
+#include "wave.h"
 
 namespace prism {
 namespace {
@@ -89,29 +90,62 @@ __device__ inline uint64_t order_of(double v) {
   return (b >> 63) ? ~b : (b | 0x8000000000000000u);
 }
 
-__device__ inline double readlane(double v, int lane) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+__device__ inline float of_order(uint32_t o) {
+  return __builtin_bit_cast(float, (o >> 31) ? (o & 0x7fffffffu) : ~o);
+}
+
+template <typename K>
+__device__ inline K readlane(K v, int lane) {
+  if constexpr (sizeof(K) == 4) {
+    return (K)__builtin_amdgcn_readlane((int)v, lane);
+  } else {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+    return ((uint64_t)hi << 32) | lo;
+  }
 }
 
 __device__ inline double sigmoid(double z) { return 1.0 / (1.0 + exp(-z)); }
+// Within 2^-20, for keys that are looked at again.
+__device__ inline float near_exp(float z) { return __builtin_amdgcn_exp2f(z * 0x1.715476p+0f); }
+__device__ inline float near_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + near_exp(-z)); }
+constexpr float kNear = 0x1p-17f;
+
+// A wave's LDS: what it ranks, and the choices in their order.
+struct Ranked {
+  float z[64];
+  uint16_t expert[64];
+};
 
 // One token's choice by a wave.  Lane j < top gets choice j (-1: none left) and its weight.
+//
+// A bound that at least `top` lanes' largest keys reach is found bit by bit.  The
+// keys that reach it, a few more than `top`, go to one lane each and are ranked, by
+// key and then by index.  With a bias the bound is one on keys in fp32, lowered by
+// more than their error, and only what reaches it has its key computed in 64 bits
+// (8192 x 256, top 8: that and the ranking for a maximum over the lanes for each
+// choice, with all keys in 64 bits, 20 us).  More keys than lanes, in rows of many
+// equal or few open ones, are chosen by such maxima.
 template <typename T, int V, bool BIAS>
-__device__ inline void choose(const Route& a, int row, int& id, float& weight) {
+__device__ inline void choose(const Route& a, int row, Ranked& lds, int& id, float& weight) {
   using Key = typename std::conditional<BIAS, uint64_t, uint32_t>::type;
   const int lane = threadIdx.x & 63;
-  const T* zp = static_cast<const T*>(a.logits) + (int64_t)row * a.ld;
+  const T* zp = static_cast<const T*>(a.logits) + (int64_t)row * a.ld + lane * V;
   const float kInf = __builtin_inff();
   float z[V];
+  if (a.E == 64 * V) {
+    T t[V];
+    __builtin_memcpy(t, zp, sizeof(t));  // rows start at any element
+#pragma unroll
+    for (int v = 0; v < V; ++v) z[v] = (float)t[v];
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) z[v] = lane * V + v < a.E ? (float)zp[v] : -kInf;
+  }
   bool bad = false;
   float most = -kInf;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = lane * V + v;
-    z[v] = e < a.E ? (float)zp[e] : -kInf;
     bad = bad || !(z[v] < kInf);  // NaN or +inf
     most = fmaxf(most, z[v]);
   }
@@ -122,60 +156,120 @@ __device__ inline void choose(const Route& a, int row, int& id, float& weight) {
     return;
   }
   const bool softmax = a.score == PRISM_SCORE_SOFTMAX;
-  double shift = 0.0, total = 1.0;  // of the softmax
-  double s[V];
+  float shift = 0.0f;   // of the softmax
+  double total = 1.0;
   if (softmax) {
-    const uint32_t m = wave_max(order_of(most));
-    const float f = __builtin_bit_cast(float, (m >> 31) ? (m & 0x7fffffffu) : ~m);
-    if (f > -kInf) shift = (double)f;
-  }
-  if (BIAS || (softmax && !a.renormalize)) {
-    double mine = 0.0;
+    const float f = of_order(wave_max(order_of(most)));
+    if (f > -kInf) shift = f;
+    if (BIAS || !a.renormalize) {
+      double mine = 0.0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[v] = softmax ? exp((double)z[v] - shift) : sigmoid((double)z[v]);
-      mine += s[v];
+      for (int v = 0; v < V; ++v) mine += exp((double)z[v] - (double)shift);
+      total = wave_sum(mine);
     }
-    if (softmax) total = wave_sum(mine);
   }
-  Key key[V];
+  auto score_of = [&](float zv) { return softmax ? exp((double)zv - (double)shift) / total : sigmoid((double)zv); };
+  auto key_of = [&](float zv, int e) -> Key {
+    if constexpr (BIAS) {
+      const double k = score_of(zv) + (double)a.bias[e];
+      return zv > -kInf && k > -__builtin_inf() ? order_of(k) : 0;
+    } else {
+      return zv > -kInf ? order_of(zv) : 0;
+    }
+  };
+  // keys in fp32, 0 for what is closed, and the bound on them
+  uint32_t near[V], largest = 0;
+  const float over = softmax ? 1.0f / (float)total : 1.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
+    near[v] = z[v] > -kInf ? order_of(z[v]) : 0;
     if constexpr (BIAS) {
       const int e = lane * V + v;
-      const double k = (softmax ? s[v] / total : s[v]) + (e < a.E ? (double)a.bias[e] : 0.0);
-      key[v] = z[v] > -kInf && k > -__builtin_inf() ? order_of(k) : 0;
-    } else {
-      key[v] = z[v] > -kInf ? order_of(z[v]) : 0;
+      const float k = (softmax ? near_exp(z[v] - shift) * over : near_sigmoid(z[v])) + (e < a.E ? a.bias[e] : 0.0f);
+      near[v] = near[v] && k > -kInf ? order_of(k) : 0;
     }
+    largest = max(largest, near[v]);
   }
-  double score = 0.0;
-  for (int j = 0; j < a.top; ++j) {
-    Key local = key[0];
+  uint32_t bound = 0;
+  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+    const int reach = __popcll(__ballot(largest >= (bound | bit)));
+    if (reach >= a.top) bound |= bit;
+    if (reach == a.top) break;
+  }
+  if (BIAS && bound) {
+    const float f = of_order(bound);
+    // NaN where f is infinite or of no finite key: all open experts
+    const float low = f - (__builtin_fabsf(f) * kNear + kNear);
+    bound = low == low ? order_of(low) : 0;
+  }
+  bound = max(bound, 1u);
+  int count = 0;
 #pragma unroll
-    for (int v = 1; v < V; ++v) local = key[v] > local ? key[v] : local;
-    const Key best = wave_max(local);
-    if (best == 0) break;
-    const int holder = (int)__builtin_ctzll(__ballot(local == best));
-    int which = 0;
-    float value = 0.0f;
+  for (int v = 0; v < V; ++v) {
+    const uint64_t in = __ballot(near[v] >= bound);
+    const int at = count + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(in >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in, 0));
+    if (near[v] >= bound && at < 64) {
+      lds.z[at] = z[v];
+      lds.expert[at] = (uint16_t)(lane * V + v);
+    }
+    count += __popcll(in);
+  }
+  float mine = 0.0f;
+  if (count <= 64) {
+    wave_order();
+    const bool live = lane < count;
+    const float zv = live ? lds.z[lane] : 0.0f;
+    const int e = live ? lds.expert[lane] : 0;
+    const Key key = live ? key_of(zv, e) : 0;
+    int rank = 0;
+    for (int j = 0; j < count; ++j) {
+      const Key other = readlane(key, j);
+      const int oe = __builtin_amdgcn_readlane(e, j);
+      rank += other > key || (other == key && oe < e) ? 1 : 0;
+    }
+    wave_order();
+    const int chosen = __popcll(__ballot(live && key != 0 && rank < a.top));
+    if (live && key != 0 && rank < a.top) {
+      lds.z[rank] = zv;
+      lds.expert[rank] = (uint16_t)e;
+    }
+    wave_order();
+    if (lane < chosen) {
+      mine = lds.z[lane];
+      id = lds.expert[lane];
+    }
+    wave_order();
+  } else {
+    Key key[V];
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) {
-        which = v;
-        value = z[v];
+    for (int v = 0; v < V; ++v) key[v] = key_of(z[v], min(lane * V + v, a.E - 1));
+    for (int j = 0; j < a.top; ++j) {
+      Key local = key[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) local = key[v] > local ? key[v] : local;
+      const Key best = wave_max(local);
+      if (best == 0) break;
+      const int holder = (int)__builtin_ctzll(__ballot(local == best));
+      int which = 0;
+      float value = 0.0f;
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v)
+        if (key[v] == best) {
+          which = v;
+          value = z[v];
+        }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (lane == holder && v == which) key[v] = 0;
+      const int e = holder * V + __builtin_amdgcn_readlane(which, holder);
+      const float zv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, value), holder));
+      if (lane == j) {
+        id = e;
+        mine = zv;
       }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane == holder && v == which) key[v] = 0;
-    const int e = holder * V + __builtin_amdgcn_readlane(which, holder);
-    const float zv = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, value), holder));
-    if (lane == j) {
-      id = e;
-      score = (double)zv;
     }
   }
-  if (id >= 0) score = softmax ? exp(score - shift) / total : sigmoid(score);
+  double score = id >= 0 ? score_of(mine) : 0.0;
   if (a.renormalize) {
     const double sum = wave_sum(score);
     score = sum > 0.0 ? score / sum : 0.0;
@@ -183,11 +277,14 @@ __device__ inline void choose(const Route& a, int row, int& id, float& weight) {
   weight = (float)(score * (double)a.scale);
 }
 
+// Experts' counts of a workgroup, whole fours of them.
+__host__ __device__ inline int pitch_of(int E) { return (E + 3) / 4 * 4; }
+constexpr int kGroups = 32;  // threads that share the workgroups' counts of an expert
+
 // What the workgroups of both launches hold.
 struct Shared {
   uint32_t mask[PRISM_EXPERTS_MAX];  // the pass's tokens of each expert
   int base[PRISM_EXPERTS_MAX];       // each expert's next place
-  int part[2][kThreads];
   int waves[kWaves];
   uint16_t id[kTokens * PRISM_TOP_MAX];
 };
@@ -206,12 +303,12 @@ __device__ inline int block_exclusive(Shared& s, int v) {
 
 // The tokens of the pass that starts at `first`, chosen by the waves.
 template <typename T, int V, bool BIAS>
-__device__ inline void route_pass(const Route& a, Shared& s, int first) {
-  const int lane = threadIdx.x & 63;
-  for (int r = (int)threadIdx.x / 64; r < kTokens && first + r < a.M; r += kWaves) {
+__device__ inline void route_pass(const Route& a, Shared& s, Ranked* ranked, int first) {
+  const int lane = threadIdx.x & 63, wave = (int)threadIdx.x / 64;
+  for (int r = wave; r < kTokens && first + r < a.M; r += kWaves) {
     int id;
     float weight;
-    choose<T, V, BIAS>(a, first + r, id, weight);
+    choose<T, V, BIAS>(a, first + r, ranked[wave], id, weight);
     if (lane < a.top) {
       const int64_t at = (int64_t)(first + r) * a.top + lane;
       a.ids[at] = id;
@@ -264,13 +361,14 @@ __device__ inline void fill_rest(const Route& a, int used) {
 template <typename T, int V, bool BIAS, bool ONE>
 __global__ __launch_bounds__(kThreads) void route_kernel(const Route a) {
   __shared__ Shared s;
+  __shared__ Ranked ranked[kWaves];
   const int t = (int)threadIdx.x;
   int count = 0;
   for (int p = 0; p < a.passes; ++p) {
     const int first = ((int)blockIdx.x * a.passes + p) * kTokens;
     s.mask[t] = 0;
     __syncthreads();
-    if (first < a.M) route_pass<T, V, BIAS>(a, s, first);
+    if (first < a.M) route_pass<T, V, BIAS>(a, s, ranked, first);
     __syncthreads();
     count += __popc(s.mask[t]);
   }
@@ -279,32 +377,45 @@ __global__ __launch_bounds__(kThreads) void route_kernel(const Route a) {
     place_pass(a, s, 0);
     fill_rest(a, used);
   } else {
-    if (t < a.E) a.counts[(int64_t)blockIdx.x * a.E + t] = (uint16_t)count;
+    if (t < pitch_of(a.E)) a.counts[(int64_t)blockIdx.x * pitch_of(a.E) + t] = t < a.E ? (uint16_t)count : 0;
   }
 }
 
+// Thread (g, c) adds up experts 4 c .. 4 c + 3 of workgroups g, g + groups, ...: of
+// those in front of this one, and of all.
 __global__ __launch_bounds__(kThreads) void place_kernel(const Route a) {
   __shared__ Shared s;
-  const int t = (int)threadIdx.x, chunk = (int)blockIdx.x;
-  // group g of the threads adds up workgroups g, g + groups, ...
-  const int wide = (a.E + 63) / 64 * 64, groups = kThreads / wide;
-  const int g = t / wide, e = t - g * wide;
-  int before = 0, total = 0;
-  if (g < groups && e < a.E) {
-    for (int c = g; c < (int)gridDim.x; c += groups) {
-      const int n = a.counts[(int64_t)c * a.E + e];
-      total += n;
-      if (c < chunk) before += n;
+  __shared__ __attribute__((aligned(16))) int part[2][4 * kThreads];
+  const int t = (int)threadIdx.x, chunk = (int)blockIdx.x, chunks = (int)gridDim.x;
+  const int pitch = pitch_of(a.E), columns = pitch / 4, groups = min(kThreads / columns, kGroups);
+  const int g = t / columns, c = t - g * columns;
+  if (g < groups) {
+    v4i before{0, 0, 0, 0}, total{0, 0, 0, 0};
+    const uint16_t* p = a.counts + 4 * c;
+    constexpr int kDeep = 8;
+    for (int w0 = g; w0 < chunks; w0 += groups * kDeep) {
+      v2i n[kDeep];
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const int w = w0 + groups * i;
+        n[i] = w < chunks ? *reinterpret_cast<const v2i*>(p + (int64_t)w * pitch) : v2i{0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const v4i four{n[i][0] & 0xffff, (int)((uint32_t)n[i][0] >> 16), n[i][1] & 0xffff, (int)((uint32_t)n[i][1] >> 16)};
+        total += four;
+        if (w0 + groups * i < chunk) before += four;
+      }
     }
+    *reinterpret_cast<v4i*>(&part[0][g * pitch + 4 * c]) = before;
+    *reinterpret_cast<v4i*>(&part[1][g * pitch + 4 * c]) = total;
   }
-  s.part[0][t] = before;
-  s.part[1][t] = total;
   __syncthreads();
-  before = total = 0;
+  int before = 0, total = 0;
   if (t < a.E) {
     for (int i = 0; i < groups; ++i) {
-      before += s.part[0][i * wide + t];
-      total += s.part[1][i * wide + t];
+      before += part[0][i * pitch + t];
+      total += part[1][i * pitch + t];
     }
   }
   const int used = start(a, s, total, before, chunk == 0);
@@ -447,7 +558,7 @@ int launch_combine(const void* x, const float* weights, const int32_t* slots, co
 
 int64_t route_experts_bytes(int64_t M, int64_t E) {
   const int64_t chunks = chunks_of(M);
-  return chunks <= 1 ? 0 : chunks * E * (int64_t)sizeof(uint16_t);
+  return chunks <= 1 ? 0 : chunks * pitch_of((int)E) * (int64_t)sizeof(uint16_t);
 }
 
 int launch_route_experts(const void* logits, int type, int64_t ld, const float* bias, int score, int renormalize,
