@@ -477,15 +477,19 @@ int launch_bias(const Route& a, hipStream_t st) {
 
 // y[m] = add[m] + sum over j ascending of weights[m][j] x[slots[m][j]], in fp32.
 // Bound by reading x: a thread takes eight columns of a row and has up to eight
-// rows of x on their way.
+// rows of x on their way.  Rows of 512 columns or more have workgroups of their own
+// (8192 x 8 of 5120 bf16, us: 178, threads numbered through all rows 197).  An x
+// larger than the cache behind the L2s is read, and y written, past it (that one 166;
+// but 3000 x 6 of 1021, 37 MB just written, 14.5, past the cache 18.9).
 constexpr int kAhead = 8;
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 
-template <typename T>
+template <bool STREAM, typename T>
 __device__ inline void load_part(const T* p, int n, float* v) {
-  typedef T v8 __attribute__((ext_vector_type(8)));
+  typedef T v8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));  // rows start anywhere
   if (n >= 8) {
-    v8 t;
-    __builtin_memcpy(&t, p, sizeof(t));  // rows start anywhere
+    const v8* p8 = reinterpret_cast<const v8*>(p);
+    const v8 t = STREAM ? __builtin_nontemporal_load(p8) : *p8;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
   } else {
@@ -494,16 +498,26 @@ __device__ inline void load_part(const T* p, int n, float* v) {
   }
 }
 
-template <typename T, typename OUT>
-__global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ x, const float* __restrict__ weights,
+// ROW: a workgroup's threads are in one row, whose slots and weights are then
+// scalars.
+template <typename T, typename OUT, bool ROW, bool STREAM>
+__global__ __launch_bounds__(1024) void combine_kernel(const T* __restrict__ x, const float* __restrict__ weights,
                                                       const int32_t* __restrict__ slots, const OUT* add, OUT* y,
-                                                      int R, int M, int top, int N, uint32_t per_row) {
-  const uint32_t at = blockIdx.x * 256u + threadIdx.x;
-  const int m = (int)(at / per_row), n = (int)(at % per_row) * 8;
-  if (m >= M) return;
+                                                      int R, int M, int top, int N, uint32_t per_row, uint32_t parts) {
+  int m, n;
+  if (ROW) {
+    m = (int)(blockIdx.x / parts);
+    n = (int)(blockIdx.x % parts * blockDim.x + threadIdx.x) * 8;
+    if (n >= N) return;
+  } else {
+    const uint32_t at = blockIdx.x * 256u + threadIdx.x;
+    m = (int)(at / per_row);
+    n = (int)(at % per_row) * 8;
+    if (m >= M) return;
+  }
   float acc[8];
   if (add) {
-    load_part(add + (int64_t)m * N + n, N - n, acc);
+    load_part<STREAM>(add + (int64_t)m * N + n, N - n, acc);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
@@ -517,7 +531,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ x, c
       const int slot = in ? slots[i] : -1;
       w[j] = in ? weights[i] : 0.0f;
       if ((uint32_t)slot < (uint32_t)R) {
-        load_part(x + (int64_t)slot * N + n, N - n, v[j]);
+        load_part<STREAM>(x + (int64_t)slot * N + n, N - n, v[j]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] = 0.0f;
@@ -532,11 +546,12 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ x, c
   }
   OUT* yp = y + (int64_t)m * N + n;
   if (N - n >= 8) {
-    typedef OUT v8 __attribute__((ext_vector_type(8)));
+    typedef OUT v8 __attribute__((ext_vector_type(8), aligned(sizeof(OUT))));
     v8 o;
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = (OUT)acc[e];
-    __builtin_memcpy(yp, &o, sizeof(o));
+    if (STREAM) __builtin_nontemporal_store(o, reinterpret_cast<v8*>(yp));
+    else *reinterpret_cast<v8*>(yp) = o;
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -544,13 +559,32 @@ __global__ __launch_bounds__(256) void combine_kernel(const T* __restrict__ x, c
   }
 }
 
+// Threads of a row, in how many workgroups of how many threads.
+struct RowGroups {
+  int64_t per_row, parts, threads;
+};
+RowGroups row_groups(int64_t N) {
+  const int64_t per_row = (N + 7) / 8, parts = (per_row + 1023) / 1024;
+  return {per_row, parts, ((per_row + parts - 1) / parts + 63) / 64 * 64};
+}
+
 template <typename T, typename OUT>
 int launch_combine(const void* x, const float* weights, const int32_t* slots, const void* add, void* y, int R, int M,
                    int top, int N, hipStream_t st) {
-  const uint32_t per_row = (uint32_t)(N + 7) / 8;
-  combine_kernel<T, OUT><<<(unsigned)(combine_threads(M, N) / 256), 256, 0, st>>>(
-      static_cast<const T*>(x), weights, slots, static_cast<const OUT*>(add), static_cast<OUT*>(y), R, M, top, N,
-      per_row);
+  const RowGroups g = row_groups(N);
+  const T* xp = static_cast<const T*>(x);
+  const OUT* ap = static_cast<const OUT*>(add);
+  OUT* yp = static_cast<OUT*>(y);
+  const bool stream = (int64_t)M * top * N * (int64_t)sizeof(T) >= kCacheBytes;
+  if (g.per_row >= 64 && stream)
+    combine_kernel<T, OUT, true, true><<<(unsigned)(M * g.parts), (unsigned)g.threads, 0, st>>>(
+        xp, weights, slots, ap, yp, R, M, top, N, (uint32_t)g.per_row, (uint32_t)g.parts);
+  else if (g.per_row >= 64)
+    combine_kernel<T, OUT, true, false><<<(unsigned)(M * g.parts), (unsigned)g.threads, 0, st>>>(
+        xp, weights, slots, ap, yp, R, M, top, N, (uint32_t)g.per_row, (uint32_t)g.parts);
+  else
+    combine_kernel<T, OUT, false, false><<<(unsigned)((M * g.per_row + 255) / 256), 256, 0, st>>>(
+        xp, weights, slots, ap, yp, R, M, top, N, (uint32_t)g.per_row, 1);
   return launch_status();
 }
 
@@ -571,7 +605,10 @@ int launch_route_experts(const void* logits, int type, int64_t ld, const float* 
   return launch_bias<__bf16>(a, st);
 }
 
-int64_t combine_threads(int64_t M, int64_t N) { return (M * ((N + 7) / 8) + 255) / 256 * 256; }
+int64_t combine_threads(int64_t M, int64_t N) {
+  const RowGroups g = row_groups(N);
+  return g.per_row >= 64 ? M * g.parts * g.threads : (M * g.per_row + 255) / 256 * 256;
+}
 
 int launch_combine_experts(const void* x, int type, const float* weights, const int32_t* slots, const void* add,
                            void* y, int y_type, int R, int M, int top, int N, hipStream_t st) {

@@ -278,6 +278,27 @@ def test_combine_rows_do_not_depend_on_the_batch():
         assert torch.equal(part, whole[lo:hi])
 
 
+@pytest.mark.parametrize("kind,n", [("bf16", 8200), ("f16", 8197), ("f32", 4100)])
+def test_combine_of_more_than_the_caches_hold(kind, n):
+    """Over 256 MB of x: whole numbers and weights that are powers of two, exact in any order."""
+    m, top = 2100, 8
+    g = torch.Generator(device=DEV).manual_seed(n)
+    x = torch.randint(-3, 4, (m * top, n), generator=g, device=DEV).to(TYPES[kind])
+    assert x.numel() * x.element_size() > 2 ** 28
+    w = torch.exp2(torch.randint(-1, 2, (m, top), generator=g, device=DEV).float())
+    slots = torch.randperm(m * top, generator=g, device=DEV).view(m, top).to(torch.int32)
+    slots[::5, 3] = -1
+    add = torch.randint(-3, 4, (m, n), generator=g, device=DEV).to(TYPES[kind])
+    want = add.float()
+    for j in range(top):
+        part = x[slots[:, j].clamp(min=0).long()].float() * w[:, j, None]
+        want += torch.where(slots[:, j, None] >= 0, part, 0.0)
+    y = add.clone()
+    assert prism.combine_experts(x, w, slots, add=y, y=y) is y
+    assert torch.equal(y, want.to(TYPES[kind]))
+    assert torch.equal(prism.combine_experts(x, w, slots, add=add), y)
+
+
 def test_combine_past_32_bit_offsets():
     r, n = 131200, 16500
     assert r * n > 2 ** 31
