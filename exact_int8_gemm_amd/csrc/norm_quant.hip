@@ -31,13 +31,14 @@ __device__ inline void load8_of(const void* p, int type, int64_t at, float* x) {
   else load8(static_cast<const __bf16*>(p) + at, x);
 }
 
-template <typename T>
+template <bool PAST, typename T>
 __device__ inline void store8(T* p, const float* x) {
   typedef T v8 __attribute__((ext_vector_type(8)));
   v8 o;
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = (T)x[e];
-  *reinterpret_cast<v8*>(p) = o;
+  if (PAST) __builtin_nontemporal_store(o, reinterpret_cast<v8*>(p));
+  else *reinterpret_cast<v8*>(p) = o;
 }
 
 constexpr int kMaxWaves = 16;
@@ -59,9 +60,14 @@ struct Norm {
   int K;
 };
 
-// T: x's type and norm's; TR: the residual's.
-template <typename T, typename TR, bool RES, bool INT8, int C>
-__global__ __launch_bounds__(C < 8 ? 512 : 1024) void norm_kernel(const Norm a) {
+// A residual of this many bytes is written past the caches: it is read again behind a whole part of the
+// layer, whose weights alone are more than the caches hold (8192 x 5120, us: fp32
+// residual 80.5, through them 84.7; bf16, 84 MB, 54 both ways).
+constexpr int64_t kPastBytes = (int64_t)128 << 20;
+
+// T: x's type and norm's; TR: the residual's, PAST: it is written past the caches.
+template <typename T, typename TR, bool RES, bool PAST, bool INT8, int C>
+__global__ __launch_bounds__(C == 1 ? 512 : 1024) void norm_kernel(const Norm a) {
   __shared__ double sums[kMaxWaves];
   __shared__ uint32_t peaks[kMaxWaves];
   const int64_t row = blockIdx.x;
@@ -87,7 +93,7 @@ __global__ __launch_bounds__(C < 8 ? 512 : 1024) void norm_kernel(const Norm a) 
   for (int i = 0; i < C; ++i) {
     const int k = ((int)threadIdx.x + threads * i) * 8;
     if constexpr (RES) {
-      if (a.residual_out && k < a.K) store8(static_cast<TR*>(a.residual_out) + row * a.out_ld + k, v[i]);
+      if (a.residual_out && k < a.K) store8<PAST>(static_cast<TR*>(a.residual_out) + row * a.out_ld + k, v[i]);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)v[i][e], (double)v[i][e], sum);
@@ -108,7 +114,7 @@ __global__ __launch_bounds__(C < 8 ? 512 : 1024) void norm_kernel(const Norm a) 
     load8_of(a.gain, a.gain_type, k, g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * inv * g[e];
-    if (a.norm) store8(static_cast<T*>(a.norm) + row * a.K + k, v[i]);
+    if (a.norm) store8<false>(static_cast<T*>(a.norm) + row * a.K + k, v[i]);
   }
   if constexpr (INT8) {
     uint32_t peak = 0;
@@ -151,21 +157,20 @@ __global__ __launch_bounds__(C < 8 ? 512 : 1024) void norm_kernel(const Norm a) 
   }
 }
 
-template <typename T, typename TR, bool RES, bool INT8>
+// Chunks of a thread: one up to 512 threads, two up to 1024 (1999 x 9680 fp16: 33.9
+// us, four of 320 threads 36.8), eight for the longest rows.
+template <typename T, typename TR, bool RES, bool PAST, bool INT8>
 int launch_chunks(const Norm& a, hipStream_t st) {
   const int chunks = a.K / 8;
   auto threads = [&](int c) { return (chunks + 64 * c - 1) / (64 * c) * 64; };
 #define PRISM_NORM(C)                                                             \
-  norm_kernel<T, TR, RES, INT8, C><<<(unsigned)a.M, threads(C), 0, st>>>(a);     \
+  norm_kernel<T, TR, RES, PAST, INT8, C><<<(unsigned)a.M, threads(C), 0, st>>>(a);     \
   return launch_status()
   if (threads(1) <= 512) {
     PRISM_NORM(1);
   }
-  if (threads(2) <= 512) {
+  if (threads(2) <= 1024) {
     PRISM_NORM(2);
-  }
-  if (threads(4) <= 512) {
-    PRISM_NORM(4);
   }
   PRISM_NORM(8);
 #undef PRISM_NORM
@@ -173,11 +178,13 @@ int launch_chunks(const Norm& a, hipStream_t st) {
 
 template <typename T, bool INT8>
 int launch_residual(const Norm& a, int res_type, hipStream_t st) {
-  if (!a.residual) return launch_chunks<T, T, false, INT8>(a, st);
+  if (!a.residual) return launch_chunks<T, T, false, false, INT8>(a, st);
+  const bool past = a.M * a.K * (res_type == PRISM_TYPE_F32 ? 4 : 2) >= kPastBytes;
   if constexpr (!__is_same(T, float)) {
-    if (res_type != PRISM_TYPE_F32) return launch_chunks<T, T, true, INT8>(a, st);
+    if (res_type != PRISM_TYPE_F32)
+      return past ? launch_chunks<T, T, true, true, INT8>(a, st) : launch_chunks<T, T, true, false, INT8>(a, st);
   }
-  return launch_chunks<T, float, true, INT8>(a, st);
+  return past ? launch_chunks<T, float, true, true, INT8>(a, st) : launch_chunks<T, float, true, false, INT8>(a, st);
 }
 
 template <bool INT8>

@@ -289,7 +289,7 @@ def test_combine_of_more_than_the_caches_hold(kind, n):
     slots = torch.randperm(m * top, generator=g, device=DEV).view(m, top).to(torch.int32)
     slots[::5, 3] = -1
     add = torch.randint(-3, 4, (m, n), generator=g, device=DEV).to(TYPES[kind])
-    want = add.float()
+    want = add.float().clone()
     for j in range(top):
         part = x[slots[:, j].clamp(min=0).long()].float() * w[:, j, None]
         want += torch.where(slots[:, j, None] >= 0, part, 0.0)
