@@ -6,41 +6,17 @@
 // The groups are known on the device only: the grid is the largest number of row
 // tiles that the sizes allow, each workgroup finds its tile from the offsets, and
 // those past the last one leave at once.
-#include "gemm_fp8_kernels.h"
+#include "gemm_fp8_grouped_wide.h"
 
 namespace prism {
 namespace {
 
 using namespace fp8;
 
-// Operands of a call.
-struct Grouped {
-  const uint8_t* q;
-  const float* s_a;
-  const int32_t* rows;     // of q, of each row of y; or null: the same one
-  const int32_t* offsets;
-  const uint8_t* w;
-  const float* s_w;
-  void* y;
-  int M, R, E, N, K;       // M: rows of q, R: of y
-};
-
-__device__ inline int wave_inclusive(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
-  return v;
-}
-
-// An expert's rows of y, and how many tiles of BM rows they make.  Whatever the
-// offsets hold, they are rows of y.
+// Tiles of BM rows that expert e's rows lo .. hi - 1 make.
 template <int BM>
 __device__ inline int tiles_of(const Grouped& a, int e, int& lo, int& hi) {
-  lo = e < a.E ? min(max(a.offsets[e], 0), a.R) : 0;
-  hi = e < a.E ? min(max(a.offsets[e + 1], lo), a.R) : 0;
+  rows_of(a, e, lo, hi);
   return (hi - lo + BM - 1) / BM;
 }
 
@@ -245,12 +221,25 @@ int launch_tile(const Grouped& a, hipStream_t st, bool check) {
   return launch_status();
 }
 
+template <typename OUT>
+int launch_wide(const Grouped& a, hipStream_t st, bool check) {
+  const int64_t tiles_n = ceil_div(a.N, wide::kColumns);
+  if (check) return PRISM_OK;
+  constexpr unsigned kGroups = 8 * wide::kSlots;
+  if (a.rows)
+    wide::grouped_wide_kernel<OUT, true><<<kGroups, 64 * wide::kWaves, 0, st>>>(a, (int)tiles_n);
+  else
+    wide::grouped_wide_kernel<OUT, false><<<kGroups, 64 * wide::kWaves, 0, st>>>(a, (int)tiles_n);
+  return launch_status();
+}
+
 template <typename OUT, bool EXACT>
 int launch(const Grouped& a, hipStream_t st, bool check) {
   const int64_t mean = a.R / (a.R < a.E ? a.R : a.E);
   if (mean <= 16) return launch_small<OUT, EXACT, 1, 1, 4>(a, st, check);
   if (mean <= 64) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
   if constexpr (!EXACT) {
+    if (mean >= 64 && a.K >= wide::kMinK) return launch_wide<OUT>(a, st, check);
     if (mean >= 192) return launch_tile<OUT, EXACT, 4, 8, 4, 2, 4, 1>(a, st, check);
   }
   return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
