@@ -233,16 +233,45 @@ int launch_wide(const Grouped& a, hipStream_t st, bool check) {
   return launch_status();
 }
 
+// Kernel for (R, E, N), fitted on MI355X with weights from HBM (us below, K = 2560; all
+// grow alike with K).  Groups are not known here: as many as can have rows are taken to,
+// each with half a tile more than its rows fill.  Estimates count rounds of the
+// tiles that run at once:
+//  * an fp32 or f16 y: the kernel for few rows while its workgroups are few (8
+//    groups of 6 rows by 2560 columns: 14.7, 64 x 64 tiles 18.3; of 16 rows 22.4 and
+//    18.9), else 64 x 64 or 128 x 128 tiles (64 groups by 640 columns: 48 rows 35 and
+//    42, 96 rows 52 and 45, 512 rows 179 and 132);
+//  * bf16: 64 x 64 tiles, 64 x 128 tiles, 128 x 128 tiles or the wide kernel (64
+//    groups by 640: 6 rows 24.9, 26.3, 26.3 and 28.9; 64 rows 32.7, 28.9, 33.7 and 37.1;
+//    128 rows 47.6, 44.3, 36.7 and 39.8; 512 rows 138, 114, 94 and 81.  By 2560: 6 rows
+//    82, 80, 88 and 90; 512 rows 526, 443, 340 and 274).
 template <typename OUT, bool EXACT>
 int launch(const Grouped& a, hipStream_t st, bool check) {
-  const int64_t mean = a.R / (a.R < a.E ? a.R : a.E);
-  if (mean <= 16) return launch_small<OUT, EXACT, 1, 1, 4>(a, st, check);
-  if (mean <= 64) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
-  if constexpr (!EXACT) {
-    if (mean >= 64 && a.K >= wide::kMinK) return launch_wide<OUT>(a, st, check);
-    if (mean >= 192) return launch_tile<OUT, EXACT, 4, 8, 4, 2, 4, 1>(a, st, check);
+  const float R = (float)a.R, G = (float)(a.R < a.E ? a.R : a.E);
+  auto tiles = [&](int bm, int bn) {
+    const float in_column = R / (float)bm + 0.5f * G;
+    return (in_column > G ? in_column : G) * (float)ceil_div(a.N, bn);
+  };
+  const float r64 = tiles(64, 64) / 768.0f, r128 = tiles(128, 128) / 512.0f;
+  if constexpr (EXACT) {
+    const float few = tiles(16, 16);
+    if (few <= 720.0f || (few <= 1280.0f && R <= 8.0f * G)) return launch_small<OUT, EXACT, 1, 1, 4>(a, st, check);
+    const float c128 = r128 <= 0.5f ? 29.0f : r128 <= 1.0f ? 44.0f : 14.0f + 42.0f * r128;
+    if (6.0f + 24.0f * r64 < c128) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
+    return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
+  } else {
+    const float r64w = tiles(64, 128) / 512.0f, turns = tiles(wide::kRows, wide::kColumns) / 256.0f;
+    const float c64 = r64 <= 0.33f ? 22.0f : r64 <= 0.87f ? 25.0f : 9.0f + 18.3f * r64;
+    const float c64w = r64w <= 0.5f ? 24.0f : r64w <= 0.95f ? 27.0f : 9.0f + 19.0f * r64w;
+    const float c128 = r128 <= 1.0f ? 35.0f : r128 <= 2.0f ? 60.0f : 10.0f + 29.0f * r128;
+    const bool can = a.K >= wide::kMinK;
+    const float cwide = can ? 20.5f * (float)(int64_t)(2.0f * (turns > 1.0f ? turns : 1.0f) + 0.99f) : 3e38f;
+    const float best = fminf(fminf(c64, c64w), fminf(c128, cwide));
+    if (best == c64) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
+    if (best == c64w) return launch_tile<OUT, EXACT, 4, 2, 2, 3, 2, 2>(a, st, check);
+    if (best == c128) return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
+    return launch_wide<OUT>(a, st, check);
   }
-  return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
 }
 
 int dispatch(const Grouped& a, int type, hipStream_t st, bool check) {

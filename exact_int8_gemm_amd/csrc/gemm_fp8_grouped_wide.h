@@ -209,10 +209,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grouped_wide_kernel(const Grou
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint32_t m = (uint32_t)numbers[64 * c + cp.crow];
-        src.from[c] = (64 * c + cp.crow < t.rows) & (m < (uint32_t)a.M) ? m * (uint32_t)K + cp.ca : kOutOfRange;
+        src.from[c] = ((64 * c + cp.crow < t.rows) & (m < (uint32_t)a.M)) ? m * (uint32_t)K + cp.ca : kOutOfRange;
       }
       const uint32_t m = (uint32_t)numbers[cp.srow];
-      src.from_s = (cp.srow < t.rows) & (m < (uint32_t)a.M) ? m * 4u : kOutOfRange;
+      src.from_s = ((cp.srow < t.rows) & (m < (uint32_t)a.M)) ? m * 4u : kOutOfRange;
       src.scales = a.M * 4;
     } else {
       src.ra = tiled::dma::rsrc_words(a.q + (size_t)t.m0 * (size_t)K, (int64_t)t.rows * K);
