@@ -64,7 +64,7 @@ constexpr int kPitch = 16 * 8 + 16;        // of a wave's 16 rows of 64 outputs
 constexpr int kAtW = 2 * kXBuf, kAtScales = kAtW + 2 * kWBuf, kAtOut = kAtScales + 2 * kRows * 4;
 constexpr int kAtRows = kAtOut + kWaves * 16 * kPitch, kAtTiles = kAtRows + 2 * kRows * 4;
 constexpr int kLds = kAtTiles + (kMaxE + 4) * 4;
-static_assert(kLds <= 160 * 1024, "LDS");
+static_assert(kLds <= 160 * 1024 && kMaxE >= PRISM_EXPERTS_MAX, "LDS");
 
 struct Tile {
   int expert, m0, rows, n0;  // rows 0: none
@@ -98,8 +98,9 @@ __device__ inline void copy4(const v4i rsrc, uint32_t to, uint32_t from) {
   (void)m0;
 }
 
+// `most`: row tiles that groups in order can have; most * tiles_n fits 31 bits.
 template <typename OUT, bool GATHER>
-__global__ __launch_bounds__(64 * kWaves, 1) void grouped_wide_kernel(const Grouped a, int tiles_n) {
+__global__ __launch_bounds__(64 * kWaves, 1) void grouped_wide_kernel(const Grouped a, int tiles_n, int most) {
   static_assert(sizeof(OUT) == 2, "rows of 64 outputs in 128 bytes");
   constexpr int TN = 4, kB = 4, kAll = 9;  // column tiles; a wave's copies of a stage: weights, rows and scales
   __shared__ __attribute__((aligned(1024))) int8_t lds[kLds];
@@ -116,7 +117,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void grouped_wide_kernel(const Grou
     for (int e0 = 0; e0 < E; e0 += 64) {
       int lo, hi;
       rows_of(a, e0 + lane, lo, hi);
-      const int upto = sum + wave_inclusive(tiles_of_units((hi - lo + 63) / 64));
+      // descending offsets name rows more than once: no more tiles than rows in order make
+      const int upto = min(sum + wave_inclusive(tiles_of_units((hi - lo + 63) / 64)), most);
       if (e0 + lane < E) before[e0 + lane + 1] = upto;
       sum = __builtin_amdgcn_readlane(upto, 63);
     }

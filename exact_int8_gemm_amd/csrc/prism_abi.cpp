@@ -478,7 +478,7 @@ int prism_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* ro
   if (K % 16 != 0 || !aligned(q, 16) || !aligned(w, 16) || !aligned(s_a, 4) || !aligned(s_w, 4) ||
       !aligned(rows, 4) || !aligned(offsets, 4) || !aligned(y, type_size(y_type)))
     return PRISM_ERR_ALIGNMENT;
-  int st = prism::check_gemm_fp8_grouped_grid(y_type, (int)M, (int)R, (int)E, (int)N, (int)K, rows != nullptr);
+  int st = prism::check_gemm_fp8_grouped_grid(y_type, (int)R, (int)E, (int)N, (int)K);
   if (st != PRISM_OK) return st;
   if ((st = check_device()) != PRISM_OK) return st;
   return prism::launch_gemm_fp8_grouped(q, s_a, rows, offsets, w, s_w, y, y_type, (int)M, (int)R, (int)E, (int)N,

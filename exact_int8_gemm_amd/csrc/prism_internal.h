@@ -114,7 +114,7 @@ int launch_route_experts(const void* logits, int type, int64_t ld, const float* 
                          float scale, int top, int32_t* ids, float* weights, int32_t* offsets, int32_t* rows,
                          int32_t* slots, void* workspace, int M, int E, hipStream_t st);
 // PRISM_ERR_INVALID_ARG where the launch that launch_gemm_fp8_grouped chooses has too many threads.
-int check_gemm_fp8_grouped_grid(int type, int M, int R, int E, int N, int K, bool gathered);
+int check_gemm_fp8_grouped_grid(int type, int R, int E, int N, int K);
 int launch_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
                             const uint8_t* w, const float* s_w, void* y, int type, int M, int R, int E, int N, int K,
                             hipStream_t st);
