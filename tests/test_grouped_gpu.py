@@ -123,6 +123,87 @@ def test_groups_of_many_sizes(counts, n, k, gather, kind):
     assert torch.equal(bits(y), bits(dense(q, sa, w, sw, counts, kind)))
 
 
+# Sizes at which a bf16 y takes the kernel of 256-column tiles: heights of 64 to 256 rows, tiles cut in the last round,
+# one to eight rounds, an odd number of blocks, a partial last one, the fewest blocks it takes, over 64 groups.
+WIDE = [([1, 64, 65, 128, 129, 192, 193, 256, 257, 320, 449, 600, 1000, 0, 700], 2560, 656),
+        ([3000, 5, 2000], 2576, 640), ([8192], 2560, 768), ([260] * 64, 2560, 1152), ([512] * 20, 5000, 1040),
+        ([0] * 7 + [150] * 100, 2560, 656), ([200] * 300, 1280, 656), ([64, 640] * 12, 2560, 5120),
+        ([320] * 16, 2560, 1296)]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,n,k", WIDE)
+def test_wide_tiles(counts, n, k, gather):
+    r, e = sum(counts), len(counts)
+    m = r // 5 if gather else r
+    q, sa, w, sw = operands(r + k, m, e, n, k)
+    rows = torch.randint(0, m, (r,), generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).to(torch.int32)
+    off = offsets_of(counts)
+    y = prism.gemm_fp8_grouped(q, sa, w, sw, off, rows=rows if gather else None, out_dtype=torch.bfloat16)
+    again = prism.gemm_fp8_grouped(q, sa, w, sw, off, rows=rows if gather else None, out_dtype=torch.bfloat16)
+    if gather:
+        q, sa = take(q, sa, rows)
+    assert torch.equal(bits(y), bits(dense(q, sa, w, sw, counts, "bf16")))
+    assert torch.equal(bits(y), bits(again))
+
+
+@pytest.mark.parametrize("gather", [False, True])
+def test_wide_tiles_exact_and_not_outside(gather):
+    """Whole numbers, exact in any order; offsets from behind 0 to before the end, rows outside q, y at an odd element
+    with memory around it, codes at any 16 bytes with NaN around them, NaN scales and codes."""
+    counts, lead, n, k = [700, 0, 1300, 64, 1900], 37, 2569, 656
+    used, e = sum(counts), len(counts)
+    r = lead + used + 91
+    m = 900 if gather else r
+    q, sa, w, sw = operands(12, m, e, n, k, integers=True)
+    bq = torch.full((m * k + 256,), 0x7F, dtype=torch.uint8, device=DEV)
+    bw = torch.full((e * n * k + 256,), 0x7F, dtype=torch.uint8, device=DEV)
+    q1, w1 = bq[48:48 + m * k].view(m, k), bw[112:112 + e * n * k].view(e, n, k)
+    q1.copy_(q.view(torch.uint8))
+    w1.copy_(w.view(torch.uint8))
+    rows = torch.randint(-3, m + 3, (r,), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    rows = rows.to(torch.int32) if gather else torch.arange(r, dtype=torch.int32, device=DEV)
+    if gather:
+        rows[lead + 5], rows[lead + used - 1] = -2 ** 31, 2 ** 31 - 1
+    off = offsets_of(counts) + lead
+    buf = torch.full((r * n + 513,), 5.0, dtype=torch.bfloat16, device=DEV)
+    y = buf[1:1 + r * n].view(r, n)
+    prism.gemm_fp8_grouped(q1.view(prism.FP8), sa, w1.view(prism.FP8), sw, off, rows=rows if gather else None, y=y)
+    assert (buf[:1 + lead * n] == 5).all() and (buf[1 + (lead + used) * n:] == 5).all()
+    ok = (rows >= 0) & (rows < m)
+    a = (q.double() * sa.double().repeat_interleave(128, 0)[:k].t())[torch.where(ok, rows, 0).long()]
+    a = torch.where(ok[:, None], a, 0.0)
+    at = lead
+    want = []
+    for i, c in enumerate(counts):
+        b = w[i].double() * sw[i].double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+        want.append(torch.mm(a[at:at + c], b.t().contiguous()).to(torch.bfloat16))
+        at += c
+    want = torch.cat(want)
+    assert torch.equal(y[lead:lead + used], want)
+    # a NaN scale of one row of q, a NaN code of one column of an expert
+    sa[2, 7] = float("nan")
+    w1[2, n - 1, k - 1] = 0x7F
+    prism.gemm_fp8_grouped(q1.view(prism.FP8), sa, w1.view(prism.FP8), sw, off, rows=rows if gather else None, y=y)
+    bad = torch.zeros((used, n), dtype=torch.bool, device=DEV)
+    bad[(rows == 7)[lead:lead + used]] = True
+    bad[700:2000, n - 1] = True
+    got = y[lead:lead + used]
+    assert torch.equal(torch.isnan(got), bad) and torch.equal(got[~bad], want[~bad])
+
+
+def test_wide_tiles_with_descending_offsets():
+    """What is written of y is not specified; nothing else is."""
+    r, n, k, e = 5005, 2576, 656, 9
+    q, sa, w, sw = operands(13, r, e, n, k)
+    buf = torch.full((r * n + 512,), 5.0, dtype=torch.bfloat16, device=DEV)
+    for off in ([0, r, 0, r, -1, r, 3, r, 2 ** 31 - 1, 0], [r, 0, r, 0, r, 0, r, 0, r, 0], [-2 ** 31] * 9 + [2 ** 31 - 1]):
+        prism.gemm_fp8_grouped(q, sa, w, sw, torch.tensor(off, dtype=torch.int32, device=DEV), y=buf[:r * n].view(r, n))
+        assert (buf[r * n:] == 5).all()
+    want = prism.gemm_fp8_blockscale(q, sa, w[8], sw[8], out_dtype=torch.bfloat16)
+    assert torch.equal(bits(buf[:r * n].view(r, n)), bits(want))      # the last list is in order: all rows are expert 8's
+
+
 @pytest.mark.parametrize("kind", list(TYPES))
 @pytest.mark.parametrize("r", [3, 70, 900])
 def test_rows_outside_the_groups_are_left(r, kind):
