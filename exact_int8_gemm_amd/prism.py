@@ -524,43 +524,55 @@ NormQuantized = collections.namedtuple("NormQuantized", "q scale residual norm")
 Routing = collections.namedtuple("Routing", "ids weights offsets rows slots")
 
 
+# The calls below are made once a layer and token: all of a call's checks stand in one
+# condition each, and only where it fails is it found out which one it was.
+
 def _dense_or_rows(x, name):
-    """_rows, at once where x is contiguous (the checks are a third of a decode call)."""
+    """_rows, at once where x is contiguous."""
     if isinstance(x, torch.Tensor) and x.is_cuda and x.ndim == 2 and x.dtype in TYPES and x.is_contiguous():
         rows, cols = x.shape
         return x.device, rows, cols, cols
     return _rows(x, name)
 
 
+def _norm_residual(x, residual, residual_out, M, K):
+    """The row strides of residual and residual_out, which are not both contiguous, or may not fit x at all."""
+    dev = x.device
+    res_dev, rows, cols, res_ld = _rows(residual, "residual")
+    if residual.dtype is not x.dtype and residual.dtype is not torch.float32:
+        raise TypeError("residual must be float32 or %s like x, got %s" % (x.dtype, residual.dtype))
+    if (rows, cols) != (M, K) or res_dev != dev:
+        raise ValueError("residual must have shape %s on %s" % ((M, K), dev))
+    out_dev, rows, cols, out_ld = _rows(residual_out, "residual_out")
+    if residual_out.dtype is not residual.dtype or (rows, cols) != (M, K) or out_dev != dev:
+        raise ValueError("residual_out must be %s of shape %s on %s" % (residual.dtype, (M, K), dev))
+    return res_ld, out_ld
+
+
 def _add_rmsnorm(fn, int8, x, gain, eps, residual, residual_out, norm, q, scale):
     dev, M, K, ld = _dense_or_rows(x, "x")
-    dtype = x.dtype
-    if not isinstance(gain, torch.Tensor) or gain.dtype not in TYPES:
-        raise TypeError("gain must be a float32, float16 or bfloat16 tensor")
-    _is(gain, "gain", gain.dtype, (K,), dev)
+    dtype, at = x.dtype, x.get_device()
+    if not (isinstance(gain, torch.Tensor) and gain.dtype in TYPES and gain.shape == (K,) and gain.get_device() == at
+            and gain.is_contiguous()):
+        if not isinstance(gain, torch.Tensor) or gain.dtype not in TYPES:
+            raise TypeError("gain must be a float32, float16 or bfloat16 tensor")
+        _need(gain, "gain", gain.dtype, (K,), dev)
     res_ptr = out_ptr = norm_ptr = None
-    res_ld = out_ld = 0
+    res_ld = out_ld = K
     res_type = dtype
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
-    else:
-        res_dev, rows, cols, res_ld = _dense_or_rows(residual, "residual")
+    if residual is not None:
+        if residual_out is None and isinstance(residual, torch.Tensor):
+            residual_out = torch.empty(M, K, dtype=residual.dtype, device=dev)
+        if not (isinstance(residual, torch.Tensor) and isinstance(residual_out, torch.Tensor)
+                and residual.shape == (M, K) and residual_out.shape == (M, K)
+                and (residual.dtype is dtype or residual.dtype is torch.float32)
+                and residual_out.dtype is residual.dtype and residual.get_device() == at
+                and residual_out.get_device() == at and residual.is_contiguous() and residual_out.is_contiguous()):
+            res_ld, out_ld = _norm_residual(x, residual, residual_out, M, K)
         res_type = residual.dtype
-        if res_type is not dtype and res_type is not torch.float32:
-            raise TypeError("residual must be float32 or %s like x, got %s" % (dtype, res_type))
-        if rows != M or cols != K or res_dev != dev:
-            raise ValueError("residual must have shape %s on %s" % ((M, K), dev))
-        if residual_out is None:
-            residual_out = torch.empty(M, K, dtype=res_type, device=dev)
-            out_ld = K
-        elif residual_out is residual:
-            out_ld = res_ld
-        else:
-            out_dev, rows, cols, out_ld = _dense_or_rows(residual_out, "residual_out")
-            if residual_out.dtype is not res_type or rows != M or cols != K or out_dev != dev:
-                raise ValueError("residual_out must be %s of shape %s on %s" % (res_type, (M, K), dev))
         res_ptr, out_ptr = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
     if norm is False or norm is None:
         norm = None
     else:
@@ -574,11 +586,13 @@ def _add_rmsnorm(fn, int8, x, gain, eps, residual, residual_out, norm, q, scale)
         q = torch.empty(M, K, dtype=q_dtype, device=dev)
     else:
         _is(q, "q", q_dtype, (M, K), dev)
-    shape = (M,) if int8 else (_blocks(K), M)
     if scale is None:
-        scale = torch.empty(*shape, dtype=torch.float32, device=dev)
+        if int8:
+            scale = torch.empty(M, dtype=torch.float32, device=dev)
+        else:
+            scale = torch.empty((K + 127) // 128, M, dtype=torch.float32, device=dev)
     else:
-        _is(scale, "scale", torch.float32, shape, dev)
+        _is(scale, "scale", torch.float32, (M,) if int8 else (_blocks(K), M), dev)
     _launch(fn, dev, x.data_ptr(), TYPES[dtype], ld, res_ptr, res_ld, out_ptr, out_ld, TYPES[res_type],
             gain.data_ptr(), TYPES[gain.dtype], eps, norm_ptr, q.data_ptr(), scale.data_ptr(), M, K)
     return NormQuantized(q, scale, residual_out, norm)
@@ -653,14 +667,20 @@ def gemm_fp8_grouped(q, s_a, w, s_w, offsets, rows=None, y=None, out_dtype=torch
     if q.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 3:
         raise ValueError("q must be 2-D and w 3-D")
     M, K = q.shape
-    E, N, _ = w.shape
-    kb = _blocks(K)
-    _is(q, "q", FP8, (M, K), dev)
-    _is(s_a, "s_a", torch.float32, (kb, M), dev)
-    _is(w, "w", FP8, (E, N, K), dev)
-    _is(s_w, "s_w", torch.float32, (E, _blocks(N), kb), dev)
-    _is(offsets, "offsets", torch.int32, (E + 1,), dev)
+    E, N, wk = w.shape
+    kb, nb, at = (K + 127) // 128, (N + 127) // 128, q.get_device()
     R = M
+    if not (isinstance(s_a, torch.Tensor) and isinstance(s_w, torch.Tensor) and isinstance(offsets, torch.Tensor)
+            and q.dtype is FP8 and w.dtype is FP8 and s_a.dtype is torch.float32 and s_w.dtype is torch.float32
+            and offsets.dtype is torch.int32 and wk == K and s_a.shape == (kb, M) and s_w.shape == (E, nb, kb)
+            and offsets.shape == (E + 1,) and w.get_device() == at and s_a.get_device() == at
+            and s_w.get_device() == at and offsets.get_device() == at and q.is_contiguous() and w.is_contiguous()
+            and s_a.is_contiguous() and s_w.is_contiguous() and offsets.is_contiguous()):
+        _need(q, "q", FP8, (M, K), dev)
+        _need(s_a, "s_a", torch.float32, (kb, M), dev)
+        _need(w, "w", FP8, (E, N, K), dev)
+        _need(s_w, "s_w", torch.float32, (E, nb, kb), dev)
+        _need(offsets, "offsets", torch.int32, (E + 1,), dev)
     if rows is not None:
         if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
             raise ValueError("rows must be a 1-D tensor")
@@ -689,9 +709,13 @@ def combine_experts(x, weights, slots, add=None, y=None, out_dtype=None):
         raise TypeError("x must be float32, float16 or bfloat16, got %s" % (x.dtype,))
     R, N = x.shape
     M, top = slots.shape
-    _is(x, "x", x.dtype, (R, N), dev)
-    _is(weights, "weights", torch.float32, (M, top), dev)
-    _is(slots, "slots", torch.int32, (M, top), dev)
+    at = x.get_device()
+    if not (isinstance(weights, torch.Tensor) and weights.dtype is torch.float32 and slots.dtype is torch.int32
+            and weights.shape == (M, top) and weights.get_device() == at and slots.get_device() == at
+            and x.is_contiguous() and weights.is_contiguous() and slots.is_contiguous()):
+        _need(x, "x", x.dtype, (R, N), dev)
+        _need(weights, "weights", torch.float32, (M, top), dev)
+        _need(slots, "slots", torch.int32, (M, top), dev)
     dtype = out_dtype
     if dtype is None:
         dtype = getattr(add if y is None else y, "dtype", x.dtype)
