@@ -66,10 +66,24 @@ __device__ inline uint64_t wave_max(uint64_t k) {
   const uint32_t lo = wave_max((uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
   return ((uint64_t)hi << 32) | lo;
 }
+template <int CTRL, int ROWS>
+__device__ inline double dpp_add(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
 __device__ inline double wave_sum(double v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+  v = dpp_add<0x111, 0xf>(v);
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);
+  v = dpp_add<0x143, 0xc>(v);
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 __device__ inline int wave_inclusive(int v) {
 #pragma unroll
@@ -113,6 +127,7 @@ constexpr float kNear = 0x1p-17f;
 
 // A wave's LDS: what it ranks, and the choices in their order.
 struct Ranked {
+  double score[64];
   float z[64];
   uint16_t expert[64];
 };
@@ -169,9 +184,9 @@ __device__ inline void choose(const Route& a, int row, Ranked& lds, int& id, flo
     }
   }
   auto score_of = [&](float zv) { return softmax ? exp((double)zv - (double)shift) / total : sigmoid((double)zv); };
-  auto key_of = [&](float zv, int e) -> Key {
+  auto key_of = [&](float zv, double score, int e) -> Key {
     if constexpr (BIAS) {
-      const double k = score_of(zv) + (double)a.bias[e];
+      const double k = score + (double)a.bias[e];
       return zv > -kInf && k > -__builtin_inf() ? order_of(k) : 0;
     } else {
       return zv > -kInf ? order_of(zv) : 0;
@@ -190,8 +205,10 @@ __device__ inline void choose(const Route& a, int row, Ranked& lds, int& id, flo
     }
     largest = max(largest, near[v]);
   }
+  // a 16-bit logit's key has nothing of its own in the lowest bits
+  constexpr int kLowest = BIAS || sizeof(T) == 4 ? 0 : std::is_same<T, _Float16>::value ? 13 : 16;
   uint32_t bound = 0;
-  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+  for (uint32_t bit = 1u << 31; bit >= 1u << kLowest; bit >>= 1) {
     const int reach = __popcll(__ballot(largest >= (bound | bit)));
     if (reach >= a.top) bound |= bit;
     if (reach == a.top) break;
@@ -214,13 +231,14 @@ __device__ inline void choose(const Route& a, int row, Ranked& lds, int& id, flo
     }
     count += __popcll(in);
   }
-  float mine = 0.0f;
+  double score = 0.0;
   if (count <= 64) {
     wave_order();
     const bool live = lane < count;
     const float zv = live ? lds.z[lane] : 0.0f;
     const int e = live ? lds.expert[lane] : 0;
-    const Key key = live ? key_of(zv, e) : 0;
+    const double sc = score_of(zv);
+    const Key key = live ? key_of(zv, sc, e) : 0;
     int rank = 0;
     for (int j = 0; j < count; ++j) {
       const Key other = readlane(key, j);
@@ -230,19 +248,20 @@ __device__ inline void choose(const Route& a, int row, Ranked& lds, int& id, flo
     wave_order();
     const int chosen = __popcll(__ballot(live && key != 0 && rank < a.top));
     if (live && key != 0 && rank < a.top) {
-      lds.z[rank] = zv;
+      lds.score[rank] = sc;
       lds.expert[rank] = (uint16_t)e;
     }
     wave_order();
     if (lane < chosen) {
-      mine = lds.z[lane];
+      score = lds.score[lane];
       id = lds.expert[lane];
     }
     wave_order();
   } else {
     Key key[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = key_of(z[v], min(lane * V + v, a.E - 1));
+    for (int v = 0; v < V; ++v) key[v] = key_of(z[v], BIAS ? score_of(z[v]) : 0.0, min(lane * V + v, a.E - 1));
+    float mine = 0.0f;
     for (int j = 0; j < a.top; ++j) {
       Key local = key[0];
 #pragma unroll
@@ -268,8 +287,8 @@ __device__ inline void choose(const Route& a, int row, Ranked& lds, int& id, flo
         mine = zv;
       }
     }
+    score = id >= 0 ? score_of(mine) : 0.0;
   }
-  double score = id >= 0 ? score_of(mine) : 0.0;
   if (a.renormalize) {
     const double sum = wave_sum(score);
     score = sum > 0.0 ? score / sum : 0.0;
