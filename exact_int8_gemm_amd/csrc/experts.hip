@@ -7,9 +7,7 @@
 // among equal keys, their weights, and a counting sort of all choices by expert
 // that keeps the order of the tokens.  The key is the logit itself, or with a bias
 // the score plus the bias in 64 bits, where two experts that differ at all also
-// differ in the key.  One wave takes one token: lane l holds experts V l ... V l + V - 1,
-// the largest key is a maximum over the lanes, and its holder the lowest lane that
-// has it.
+// differ in the key.  One wave takes one token: lane l holds experts V l ... V l + V - 1.
 //
 // The sort works on 32 tokens at a time.  A token chooses an expert once at the
 // most, so an expert's tokens are the bits of one word, set by atomic ors whose
@@ -17,6 +15,10 @@
 // rank that of the bits below its own.  One workgroup routes `passes` times 32
 // tokens and leaves its counts per expert; a second launch adds up the counts in
 // front of each workgroup's and places the choices.
+//
+// Both are bound by latency: a wave's chain of load, bound, ranking and 64-bit
+// exponential, twice, and two dependent launches (8192 x 256 fp32, top 8, with a
+// bias: 11.8 + 6.5 us, of which the bytes are 2; 4 x 128: 4.6, one launch).
 #include <type_traits>
 
 #include "../../include/prism.h"
@@ -43,7 +45,7 @@ struct Route {
   int32_t* offsets;
   int32_t* rows;
   int32_t* slots;
-  uint16_t* counts;  // [workgroups][E]
+  uint16_t* counts;  // [workgroups][pitch_of(E)]
   int M, E, passes;
 };
 
@@ -120,7 +122,9 @@ __device__ inline K readlane(K v, int lane) {
 }
 
 __device__ inline double sigmoid(double z) { return 1.0 / (1.0 + exp(-z)); }
-// Within 2^-20, for keys that are looked at again.
+// Scores within 2^-20, for keys that are looked at again: an exponent's argument is
+// off by 2^-23 |z|, which moves a score by that times |z| exp(-|z|) at the most.  A
+// sum with a bias is rounded by 2^-24 of it; kNear is eight times both.
 __device__ inline float near_exp(float z) { return __builtin_amdgcn_exp2f(z * 0x1.715476p+0f); }
 __device__ inline float near_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + near_exp(-z)); }
 constexpr float kNear = 0x1p-17f;
