@@ -21,8 +21,8 @@
 // stage of a tall tile takes 1.7 us of 64 KB for each of 256 compute units, 9 to 10
 // TB/s out of the L2s, and that of a lower tile not much less (192 rows 1.4, 128 rows
 // 1.2): the copies bound it.  Weights from HBM add 0.4 us a stage.  Not kept: a list
-// for each height, the tall tiles first, which evens out the rounds and reads weights
-// twice (64 groups 269); lines of weights touched three stages ahead (247 against 238
+// for each height, the tall tiles first, which parts a group's tiles (64 ragged groups
+// 269); lines of weights touched three stages ahead (247 against 238
 // with 64 even groups).
 #pragma once
 
