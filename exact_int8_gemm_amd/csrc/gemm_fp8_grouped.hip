@@ -198,7 +198,8 @@ int launch_tile(const Grouped& a, hipStream_t st, bool check) {
 
 template <typename OUT>
 int launch_wide(const Grouped& a, hipStream_t st, bool check) {
-  if (check) return PRISM_OK;
+  // rows are counted in whole tiles, in 32 bits
+  if (check) return a.R <= INT32_MAX - wide::kRows ? PRISM_OK : PRISM_ERR_INVALID_ARG;
   const int tiles_n = (int)ceil_div(a.N, wide::kColumns), most = (int)most_tiles(a.R, a.E, wide::kRows);
   constexpr unsigned kGroups = 8 * wide::kSlots;
   if (a.rows)

@@ -471,8 +471,8 @@ int prism_route_experts(const void* logits, int type, int64_t ld, const float* b
  *           front of offsets[0] and from offsets[E] on are left as they are.
  * Row by row the bits of prism_gemm_fp8_blockscale with that expert's weights.
  * Offsets are taken as clamped to 0 .. R; where they descend, what is written
- * of y is not specified (nothing else is).  E up to PRISM_EXPERTS_MAX; with rows,
- * M * K below 2^31.
+ * of y is not specified (nothing else is).  E up to PRISM_EXPERTS_MAX, R up to
+ * 2^31 - 257; with rows, M * K below 2^31.
  */
 int prism_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
                            const uint8_t* w, const float* s_w, void* y, int y_type, int64_t M, int64_t R, int64_t E,

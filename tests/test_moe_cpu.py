@@ -121,6 +121,9 @@ CASES += [("prism_gemm_fp8_grouped", a, e) for a, e in [
     (_g(M=1 << 25, K=64), INVALID),                      # 2^31 codes behind row numbers
     (_g(M=1 << 25, R=1 << 25, K=64, rows=None), UNSUP),
     (_g(R=IMAX, N=IMAX, M=4), INVALID),                  # grid
+    # wide tiles: their rows are counted in whole tiles, in 32 bits
+    (_g(R=IMAX, N=256, K=640), INVALID), (_g(R=IMAX - 255, N=256, K=640), INVALID),
+    (_g(R=IMAX - 256, N=256, K=640), UNSUP),
     (_g(q=None), INVALID), (_g(sa=None), INVALID), (_g(off=None), INVALID), (_g(w=None), INVALID),
     (_g(sw=None), INVALID), (_g(y=None), INVALID),
     (_g(K=72), ALIGN), (_g(q=A + 8), ALIGN), (_g(w=A + 8), ALIGN), (_g(sa=A + 2), ALIGN), (_g(sw=A + 2), ALIGN),
