@@ -1,7 +1,8 @@
 """Ahead-of-time build of libprism.so for gfx950 (MI355X) with hipcc.
 
 Each source is compiled to an object in ``_build/`` (in parallel), then the
-objects are linked into ``exact_int8_gemm_amd/libprism.so`` in-tree.
+objects are linked into ``exact_int8_gemm_amd/libprism.so`` in-tree, once the
+wait states in their code have been looked at (wait_states.py).
 
 Flags that define results, not only speed:
   -ffp-contract=off                           no fused multiply-add except the
@@ -15,11 +16,17 @@ from __future__ import annotations
 
 import hashlib
 import os
+import shutil
 import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
+if ROOT not in sys.path:
+    sys.path.insert(0, ROOT)
+
+from exact_int8_gemm_amd import wait_states  # noqa: E402
+
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libprism.so")
@@ -28,6 +35,7 @@ SOURCES = ["quantize.hip", "gemm_small.hip", "gemm_tiled.hip", "repack.hip", "fp
            "gemm_fp8_grouped.hip", "norm_quant.hip", "experts.hip", "logprobs.hip", "peaks.hip", "prism_abi.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+OBJDUMP = os.path.join(os.path.dirname(os.path.dirname(shutil.which(HIPCC) or HIPCC)), "llvm", "bin", "llvm-objdump")
 ARCH = "gfx950"
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", "-Werror=inline-asm",
@@ -99,6 +107,11 @@ def build_library(verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    early = wait_states.check(tmp, OBJDUMP, ARCH)[1]
+    if early:
+        os.unlink(tmp)
+        raise RuntimeError("a copy into LDS comes %d wait states behind %s: %s in %s" %
+                           (early[0][4], early[0][3], early[0][2], early[0][0]))
     os.replace(tmp, LIB)
     return LIB
 

@@ -93,17 +93,19 @@ __device__ inline T scalar(const T* p, int64_t i) {
 }
 __device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// tiled::dma's copies with all but the offset in scalar registers as they come:
-// made sure of by a lane read, they would first be moved to vector registers, and
-// held there over the stages.
+// tiled::dma's copies, wait states and all, with all but the offset in scalar registers
+// as they come: made sure of by a lane read, they would first be moved to vector
+// registers, and held there over the stages.  The descriptors of the codes stay in
+// scalar registers; that of the scales comes from spilled ones, right in front of its
+// copy.
 __device__ inline void copy16(const v4i rsrc, uint32_t to, uint32_t from) {
   uint32_t m0;
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" : "={m0}"(m0) : "s"(to), "v"(from), "s"(rsrc) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" : "={m0}"(m0) : "s"(to), "v"(from), "s"(rsrc) : "memory");
   (void)m0;
 }
 __device__ inline void copy4(const v4i rsrc, uint32_t to, uint32_t from) {
   uint32_t m0;
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dword %2, %3, 0 offen lds" : "={m0}"(m0) : "s"(to), "v"(from), "s"(rsrc) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dword %2, %3, 0 offen lds" : "={m0}"(m0) : "s"(to), "v"(from), "s"(rsrc) : "memory");
   (void)m0;
 }
 

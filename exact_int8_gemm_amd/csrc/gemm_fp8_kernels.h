@@ -270,7 +270,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
     const int row = arow + 16 * TM * (c % V) + 32 * (c / V);
     const uint32_t in = GATHER ? from[GATHER ? c : 0] + ck : each_time(xoff) + ((uint32_t)(row * K) + ck);
     const uint32_t o = ca + ck < (uint32_t)K ? in : kOutOfRange;
-    tiled::dma::copy_to_lds(ra, lx0 + (uint32_t)(buf * kXBuf + row * kBlock), o);
+    tiled::dma::copy_to_lds<0>(ra, lx0 + (uint32_t)(buf * kXBuf + row * kBlock), o);
   };
   auto copy_w = [&](int i, int b, int buf) __attribute__((always_inline)) {
     const uint32_t ck = (uint32_t)b * kBlock;
@@ -278,7 +278,7 @@ __device__ __attribute__((always_inline)) inline void tile_body(int8_t* lds, con
     const uint32_t cb = NW == 4 && i % 2 == 1 ? cb1 : cb0;
     const uint32_t in = each_time(woff) + cb + ((uint32_t)(row * K) + ck);
     const uint32_t o = cb + ck < (uint32_t)K ? in : kOutOfRange;
-    tiled::dma::copy_to_lds(rb, lw0 + (uint32_t)(buf * kWBuf + row * kBlock), o);
+    tiled::dma::copy_to_lds<0>(rb, lw0 + (uint32_t)(buf * kWBuf + row * kBlock), o);
   };
   auto copy_s = [&](int b, int buf) __attribute__((always_inline)) {
     const int bb = b < KB ? b : KB - 1;

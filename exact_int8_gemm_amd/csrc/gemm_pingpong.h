@@ -185,7 +185,7 @@ __global__ __launch_bounds__(512, 1) void gemm_pp_kernel(const int8_t* __restric
       const int copy = b_copy(s - kPerWaveA);
       const uint32_t o = (blive && bk + chunk_a(copy) * 16 < KB) ? off[s] + (uint32_t)bk : kOutOfRange;
       const int8_t* dst = lds + RING * kStage + ((bk / BK) & 1) * kPair + copy * 1024;
-      copy_to_lds(wb, lds_addr(dst), o);
+      copy_to_lds<0>(wb, lds_addr(dst), o);
     }
     if (h == 1) {
       bk += BK;
@@ -218,7 +218,7 @@ __global__ __launch_bounds__(512, 1) void gemm_pp_kernel(const int8_t* __restric
       const int copy = isA ? wave * kPerWaveA + s : b_copy(s - kPerWaveA);
       const uint32_t o = (clive && ck + chunk_a(copy) * 16 < K) ? off[s] + (uint32_t)ck : kOutOfRange;
       const int8_t* dst = lds + buf * kStage + (isA ? 0 : BM * BK) + copy * 1024;
-      copy_to_lds(isA ? ca : cb, lds_addr(dst), o);
+      copy_to_lds<0>(isA ? ca : cb, lds_addr(dst), o);
     }
     if (part != kParts - 1) return;
     if constexpr (W4) issue_half_pair(h);

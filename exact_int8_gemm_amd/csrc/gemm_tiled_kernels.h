@@ -507,7 +507,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void gemm_dma_kernel(const int8_
       const int copy = isA ? wave * C::kPerWaveA + s : wave * C::kPerWaveB + (s - C::kPerWaveA);
       const uint32_t o = (k0 + kc[s] < kend) ? off[s] + (uint32_t)k0 : kOutOfRange;
       const int8_t* dst = base + (isA ? 0 : BM * BK) + copy * 1024;
-      copy_to_lds(isA ? ra : rb, lds_addr(dst), o);
+      copy_to_lds<0>(isA ? ra : rb, lds_addr(dst), o);
     }
   };
 

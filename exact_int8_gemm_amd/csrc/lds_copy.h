@@ -37,13 +37,23 @@ __device__ inline v4i rsrc_words(const void* base, int64_t bytes) {
 // not see that the statement holds an LDS DMA, so it must not be the one to
 // place the M0 write: with M0 given as an input operand it put the next
 // copy's M0 write directly behind a copy in flight, and the GPU faulted.
+//
+// Nor does it add the wait states that the hardware leaves to the program: one
+// between a scalar write of M0 and a copy into LDS, and five between a vector
+// instruction that writes a scalar register, as the lane reads here and those
+// that bring back spilled registers do, and a copy that reads it.  The M0 write
+// is one of the five, s_nop 3 the other four.  WAIT = 0 is one state, for kernels
+// that hold their descriptors in scalar registers over the loop: the build looks
+// at the code of every copy and refuses one that comes too early (8192 x 5120 x
+// 5120 int8 195 to 197 us, with 3 198 to 199; fp8 500 x 2560 x 9600 35.9 and 36.5).
+template <int WAIT = 3>
 __device__ inline void copy_to_lds(const v4i rsrc, uint32_t lds_addr, uint32_t voff) {
   // lds_addr and rsrc are wave-uniform; readfirstlane puts them in SGPRs.
   const uint32_t m0v = __builtin_amdgcn_readfirstlane(lds_addr);
   const v4i r = v4i{__builtin_amdgcn_readfirstlane(rsrc[0]), __builtin_amdgcn_readfirstlane(rsrc[1]),
                     __builtin_amdgcn_readfirstlane(rsrc[2]), __builtin_amdgcn_readfirstlane(rsrc[3])};
   uint32_t m0_out;
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" : "={m0}"(m0_out) : "s"(m0v), "v"(voff), "s"(r) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop %4\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" : "={m0}"(m0_out) : "s"(m0v), "v"(voff), "s"(r), "n"(WAIT) : "memory");
   (void)m0_out;
 }
 
@@ -54,7 +64,7 @@ __device__ inline void copy2_to_lds(const v4i rsrc, uint32_t lds_addr, uint32_t 
   const v4i r = v4i{__builtin_amdgcn_readfirstlane(rsrc[0]), __builtin_amdgcn_readfirstlane(rsrc[1]),
                     __builtin_amdgcn_readfirstlane(rsrc[2]), __builtin_amdgcn_readfirstlane(rsrc[3])};
   uint32_t m0_out;
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_ushort %2, %3, 0 offen lds" : "={m0}"(m0_out) : "s"(m0v), "v"(voff), "s"(r) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_ushort %2, %3, 0 offen lds" : "={m0}"(m0_out) : "s"(m0v), "v"(voff), "s"(r) : "memory");
   (void)m0_out;
 }
 
@@ -64,7 +74,7 @@ __device__ inline void copy4_to_lds(const v4i rsrc, uint32_t lds_addr, uint32_t 
   const v4i r = v4i{__builtin_amdgcn_readfirstlane(rsrc[0]), __builtin_amdgcn_readfirstlane(rsrc[1]),
                     __builtin_amdgcn_readfirstlane(rsrc[2]), __builtin_amdgcn_readfirstlane(rsrc[3])};
   uint32_t m0_out;
-  asm volatile("s_mov_b32 m0, %1\n\tbuffer_load_dword %2, %3, 0 offen lds" : "={m0}"(m0_out) : "s"(m0v), "v"(voff), "s"(r) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 3\n\tbuffer_load_dword %2, %3, 0 offen lds" : "={m0}"(m0_out) : "s"(m0v), "v"(voff), "s"(r) : "memory");
   (void)m0_out;
 }
 
