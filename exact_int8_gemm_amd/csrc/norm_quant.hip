@@ -163,21 +163,19 @@ __global__ __launch_bounds__(C == 1 ? 512 : 1024) void norm_kernel(const Norm a)
 
 // Chunks of a thread: one up to 512 threads, two up to 1024 (1999 x 9680 fp16: 33.9
 // us, four of 320 threads 36.8), eight for the longest rows.
+constexpr int threads_of(int64_t K, int chunks) { return (int)((K / 8 + 64 * chunks - 1) / (64 * chunks) * 64); }
+constexpr int chunks_of(int64_t K) { return threads_of(K, 1) <= 512 ? 1 : threads_of(K, 2) <= 1024 ? 2 : 8; }
+static_assert(threads_of(PRISM_NORM_K_MAX, 8) <= 1024, "the longest row");
+
 template <typename T, typename TR, bool RES, bool PAST, bool INT8>
 int launch_chunks(const Norm& a, hipStream_t st) {
-  const int chunks = a.K / 8;
-  auto threads = [&](int c) { return (chunks + 64 * c - 1) / (64 * c) * 64; };
-#define PRISM_NORM(C)                                                             \
-  norm_kernel<T, TR, RES, PAST, INT8, C><<<(unsigned)a.M, threads(C), 0, st>>>(a);     \
-  return launch_status()
-  if (threads(1) <= 512) {
-    PRISM_NORM(1);
-  }
-  if (threads(2) <= 1024) {
-    PRISM_NORM(2);
-  }
-  PRISM_NORM(8);
+#define PRISM_NORM(C) norm_kernel<T, TR, RES, PAST, INT8, C><<<(unsigned)a.M, threads_of(a.K, C), 0, st>>>(a)
+  const int chunks = chunks_of(a.K);
+  if (chunks == 1) PRISM_NORM(1);
+  else if (chunks == 2) PRISM_NORM(2);
+  else PRISM_NORM(8);
 #undef PRISM_NORM
+  return launch_status();
 }
 
 template <typename T, bool INT8>
@@ -200,7 +198,7 @@ int launch_type(const Norm& a, int x_type, int res_type, hipStream_t st) {
 
 }  // namespace
 
-int64_t norm_threads(int64_t M, int64_t K) { return M * ((K / 8 + 63) / 64 * 64); }
+int64_t norm_threads(int64_t M, int64_t K) { return M * threads_of(K, chunks_of(K)); }
 
 int launch_add_rmsnorm_quantize(const void* x, int x_type, int64_t x_ld, const void* residual, int64_t res_ld,
                                 void* residual_out, int64_t out_ld, int res_type, const void* gain, int gain_type,
