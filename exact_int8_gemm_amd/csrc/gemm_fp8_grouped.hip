@@ -221,8 +221,8 @@ int launch_wide(const Grouped& a, hipStream_t st, bool check) {
 //    groups by 640: 6 rows 24.9, 26.3, 26.3 and 28.9; 64 rows 32.7, 28.9, 33.7 and 37.1;
 //    128 rows 47.6, 44.3, 36.7 and 39.8; 512 rows 138, 114, 94 and 81.  By 2560: 6 rows
 //    82, 80, 88 and 90; 512 rows 526, 443, 340 and 274).
-template <typename OUT, bool EXACT>
-int launch(const Grouped& a, hipStream_t st, bool check) {
+template <bool EXACT>
+int form_of(const Grouped& a) {
   const float R = (float)a.R, G = (float)(a.R < a.E ? a.R : a.E);
   auto tiles = [&](int bm, int bn) {
     const float in_column = R / (float)bm + 0.5f * G;
@@ -231,10 +231,9 @@ int launch(const Grouped& a, hipStream_t st, bool check) {
   const float r64 = tiles(64, 64) / 768.0f, r128 = tiles(128, 128) / 512.0f;
   if constexpr (EXACT) {
     const float few = tiles(16, 16);
-    if (few <= 720.0f || (few <= 1280.0f && R <= 8.0f * G)) return launch_small<OUT>(a, st, check);
+    if (few <= 720.0f || (few <= 1280.0f && R <= 8.0f * G)) return PRISM_GROUPED_FEW;
     const float c128 = r128 <= 0.5f ? 29.0f : r128 <= 1.0f ? 44.0f : 14.0f + 42.0f * r128;
-    if (6.0f + 24.0f * r64 < c128) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
-    return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
+    return 6.0f + 24.0f * r64 < c128 ? PRISM_GROUPED_64x64 : PRISM_GROUPED_128x128;
   } else {
     const float r64w = tiles(64, 128) / 512.0f, turns = tiles(wide::kRows, wide::kColumns) / 256.0f;
     const float c64 = r64 <= 0.33f ? 22.0f : r64 <= 0.87f ? 25.0f : 9.0f + 18.3f * r64;
@@ -243,9 +242,20 @@ int launch(const Grouped& a, hipStream_t st, bool check) {
     const bool can = a.K >= wide::kMinK && most_tiles(a.R, a.E, wide::kRows) * ceil_div(a.N, wide::kColumns) <= INT32_MAX;
     const float cwide = can ? 20.5f * (float)(int64_t)(2.0f * (turns > 1.0f ? turns : 1.0f) + 0.99f) : 3e38f;
     const float best = fminf(fminf(c64, c64w), fminf(c128, cwide));
-    if (best == c64) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
-    if (best == c64w) return launch_tile<OUT, EXACT, 4, 2, 2, 3, 2, 2>(a, st, check);
-    if (best == c128) return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
+    return best == c64 ? PRISM_GROUPED_64x64 : best == c64w ? PRISM_GROUPED_64x128
+                                             : best == c128 ? PRISM_GROUPED_128x128 : PRISM_GROUPED_WIDE;
+  }
+}
+
+template <typename OUT, bool EXACT>
+int launch(const Grouped& a, hipStream_t st, bool check) {
+  const int form = form_of<EXACT>(a);
+  if (form == PRISM_GROUPED_64x64) return launch_tile<OUT, EXACT, 2, 2, 2, 3, 2, 3>(a, st, check);
+  if (form == PRISM_GROUPED_128x128) return launch_tile<OUT, EXACT, 2, 4, 4, 2, 2, 2>(a, st, check);
+  if constexpr (EXACT) {
+    return launch_small<OUT>(a, st, check);
+  } else {
+    if (form == PRISM_GROUPED_64x128) return launch_tile<OUT, EXACT, 4, 2, 2, 3, 2, 2>(a, st, check);
     return launch_wide<OUT>(a, st, check);
   }
 }
@@ -260,6 +270,11 @@ int dispatch(const Grouped& a, int type, hipStream_t st, bool check) {
 
 int check_gemm_fp8_grouped_grid(int type, int R, int E, int N, int K) {
   return dispatch({nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, R, E, N, K}, type, nullptr, true);
+}
+
+int gemm_fp8_grouped_form(int type, int R, int E, int N, int K) {
+  const Grouped a{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, R, E, N, K};
+  return type == PRISM_TYPE_BF16 ? form_of<false>(a) : form_of<true>(a);
 }
 
 int launch_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,

@@ -465,14 +465,24 @@ int prism_route_experts(const void* logits, int type, int64_t ld, const float* b
                                      static_cast<hipStream_t>(stream));
 }
 
+static bool grouped_sizes(int64_t R, int64_t E, int64_t N, int64_t K) {
+  return R > 0 && R <= INT_MAX && E > 0 && E <= PRISM_EXPERTS_MAX && N > 0 && N <= INT_MAX && K > 0 &&
+         K <= PRISM_K_MAX && E * N <= INT64_MAX / K;
+}
+
+int prism_gemm_fp8_grouped_form(int y_type, int64_t R, int64_t E, int64_t N, int64_t K) {
+  if (!known_type(y_type) || !grouped_sizes(R, E, N, K)) return PRISM_ERR_INVALID_ARG;
+  if (K % 16 != 0) return PRISM_ERR_ALIGNMENT;
+  const int st = prism::check_gemm_fp8_grouped_grid(y_type, (int)R, (int)E, (int)N, (int)K);
+  return st != PRISM_OK ? st : prism::gemm_fp8_grouped_form(y_type, (int)R, (int)E, (int)N, (int)K);
+}
+
 int prism_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
                            const uint8_t* w, const float* s_w, void* y, int y_type, int64_t M, int64_t R, int64_t E,
                            int64_t N, int64_t K, void* stream) {
   if (!known_type(y_type) || M < 0 || R < 0 || E < 0 || N < 0 || K < 0) return PRISM_ERR_INVALID_ARG;
   if (R == 0) return PRISM_OK;
-  if (M == 0 || M > INT_MAX || R > INT_MAX || E == 0 || E > PRISM_EXPERTS_MAX || N == 0 || N > INT_MAX || K == 0 ||
-      K > PRISM_K_MAX || E * N > INT64_MAX / K)
-    return PRISM_ERR_INVALID_ARG;
+  if (M == 0 || M > INT_MAX || !grouped_sizes(R, E, N, K)) return PRISM_ERR_INVALID_ARG;
   if (!q || !s_a || !offsets || !w || !s_w || !y) return PRISM_ERR_INVALID_ARG;
   if (rows ? M * K >= (int64_t)1 << 31 : M != R) return PRISM_ERR_INVALID_ARG;
   if (K % 16 != 0 || !aligned(q, 16) || !aligned(w, 16) || !aligned(s_a, 4) || !aligned(s_w, 4) ||

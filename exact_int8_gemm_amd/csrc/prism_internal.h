@@ -115,6 +115,7 @@ int launch_route_experts(const void* logits, int type, int64_t ld, const float* 
                          int32_t* slots, void* workspace, int M, int E, hipStream_t st);
 // PRISM_ERR_INVALID_ARG where the launch that launch_gemm_fp8_grouped chooses has too many threads.
 int check_gemm_fp8_grouped_grid(int type, int R, int E, int N, int K);
+int gemm_fp8_grouped_form(int type, int R, int E, int N, int K);  // PRISM_GROUPED_*
 int launch_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
                             const uint8_t* w, const float* s_w, void* y, int type, int M, int R, int E, int N, int K,
                             hipStream_t st);

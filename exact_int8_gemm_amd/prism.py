@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libprism.so")
 
 PRISM_OK = 0
-ABI_VERSION = 16
+ABI_VERSION = 17
 K_MAX = 131040
 
 # Dispatch-table entries of the W8A8 / W4A8 calls (PRISM_VARIANT_* in include/prism.h).
@@ -92,6 +92,8 @@ def _declare(lib):
     lib.prism_route_experts.argtypes = [p, i32, i64, p, i32, i32, ctypes.c_float, i32, p, p, p, p, p, p, i64, i64, i64, p]
     lib.prism_gemm_fp8_grouped.restype = i32
     lib.prism_gemm_fp8_grouped.argtypes = [p, p, p, p, p, p, p, i32, i64, i64, i64, i64, i64, p]
+    lib.prism_gemm_fp8_grouped_form.restype = i32
+    lib.prism_gemm_fp8_grouped_form.argtypes = [i32, i64, i64, i64, i64]
     lib.prism_combine_experts.restype = i32
     lib.prism_combine_experts.argtypes = [p, i32, p, p, p, p, i32, i64, i64, i64, i64, p]
     lib.prism_peak_mfma.restype = i32
@@ -696,6 +698,20 @@ def gemm_fp8_grouped(q, s_a, w, s_w, offsets, rows=None, y=None, out_dtype=torch
     _launch(lib().prism_gemm_fp8_grouped, dev, q.data_ptr(), s_a.data_ptr(), None if rows is None else rows.data_ptr(),
             offsets.data_ptr(), w.data_ptr(), s_w.data_ptr(), y.data_ptr(), TYPES[dtype], M, R, E, N, K)
     return y
+
+
+GROUPED_FORMS = ("few", "64x64", "64x128", "128x128", "wide")  # PRISM_GROUPED_* in include/prism.h
+
+
+def gemm_fp8_grouped_form(R, E, N, K, out_dtype=torch.float32):
+    """Name of the kernel that gemm_fp8_grouped runs for these sizes (one of ``GROUPED_FORMS``), whatever the groups are;
+    for tests and profiles.  No GPU is needed."""
+    if out_dtype not in TYPES:
+        raise TypeError("y must be float32, float16 or bfloat16, got %s" % (out_dtype,))
+    form = lib().prism_gemm_fp8_grouped_form(TYPES[out_dtype], R, E, N, K)
+    if form < 0:
+        _check(form)
+    return GROUPED_FORMS[form]
 
 
 def combine_experts(x, weights, slots, add=None, y=None, out_dtype=None):

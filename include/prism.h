@@ -44,7 +44,7 @@ extern "C" {
 #endif
 
 /* Bumped on any change of a signature or of the semantics below. */
-#define PRISM_ABI_VERSION 16
+#define PRISM_ABI_VERSION 17
 
 /* Largest accepted K.  For K <= 131040 every exact sum of K products of two
  * int8 values (|q|, |w| <= 128) lies strictly inside the int32 range. */
@@ -477,6 +477,21 @@ int prism_route_experts(const void* logits, int type, int64_t ld, const float* b
 int prism_gemm_fp8_grouped(const uint8_t* q, const float* s_a, const int32_t* rows, const int32_t* offsets,
                            const uint8_t* w, const float* s_w, void* y, int y_type, int64_t M, int64_t R, int64_t E,
                            int64_t N, int64_t K, void* stream);
+
+/*
+ * Which of its kernels such a call runs (all give the same bits), for tests and
+ * profiles; a host function, no device is looked at.  Negative status codes for
+ * sizes that the call refuses.
+ *   PRISM_GROUPED_FEW     16 x 16 tiles, of fp32 and fp16 outputs
+ *   PRISM_GROUPED_<r>x<c> LDS tiles of r rows and c columns (64x128: of bf16 only)
+ *   PRISM_GROUPED_WIDE    up to 256 rows by 256 columns, of bf16 outputs
+ */
+#define PRISM_GROUPED_FEW 0
+#define PRISM_GROUPED_64x64 1
+#define PRISM_GROUPED_64x128 2
+#define PRISM_GROUPED_128x128 3
+#define PRISM_GROUPED_WIDE 4
+int prism_gemm_fp8_grouped_form(int y_type, int64_t R, int64_t E, int64_t N, int64_t K);
 
 /*
  * A token's expert outputs added up with its weights.
