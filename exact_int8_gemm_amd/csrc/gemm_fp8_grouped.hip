@@ -69,9 +69,8 @@ __device__ inline int count_tiles(const Grouped& a) {
 // the weights once.  A workgroup owns 16 rows of a group and 16 columns, and its waves
 // share out K: in rounds of kWaves blocks, each wave multiplies its block straight from
 // global memory and leaves the sums in LDS with the blocks' scales; after one
-// barrier, threads fold the round's blocks into their outputs in order.  (A bf16 y,
-// whose operands need no conversion, takes 64 x 64 tiles at any size: 17 x 8 rows of 128
-// groups, 2560 x 4096, 109 us, so 112.)
+// barrier, threads fold the round's blocks into their outputs in order.  A bf16 y,
+// whose operands need no conversion, never takes this kernel.
 constexpr int kWaves = 4;
 template <typename OUT>
 __global__ __launch_bounds__(64 * kWaves) void grouped_small_kernel(const Grouped a, int tiles_n) {
