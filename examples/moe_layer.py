@@ -5,8 +5,10 @@
 The weights (synthetic here) are laid out once: e4m3 codes with one scale for each 128 x 128 tile of each expert's
 weights.  A layer takes the layer before's output and the residual of M tokens and
 
-    adds the residual, norms and quantizes in one pass, and keeps the norm for the router,
-    multiplies it by the router's weights, chooses each token's experts and lists the rows of each expert,
+    adds the residual, norms and quantizes in one pass,
+    multiplies the norm's e4m3 codes by the router's weights, also in e4m3, so that a token's logits have the same bits in
+    any batch (a router that is to see the norm itself takes it from the same call with norm=True, and its own product),
+    chooses each token's experts and lists the rows of each expert,
     multiplies those rows by their experts' gate and up weights, applies SwiGLU and quantizes,
     multiplies by the down weights, and adds up each token's outputs with the router's weights.
 
@@ -40,7 +42,7 @@ class Layer:
     def __init__(self, gain, router, gate_up, down, top, eps=1e-6):
         """gain [H], router [E][H] fp32, gate_up [E][2 I][H], down [E][H][I]."""
         self.gain, self.eps, self.top = gain, eps, top
-        # the router's product is one row at a time the same in any batch: fp8 with an fp32 result
+        # fp8 with an fp32 result: a product whose rows do not depend on the batch
         self.router = prism.quantize_tiles_fp8(router)
         self.gate_up, self.down = quantize_experts(gate_up), quantize_experts(down)
         self.inner = down.shape[2]
