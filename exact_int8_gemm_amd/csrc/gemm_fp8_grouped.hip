@@ -1,7 +1,8 @@
 // fp8 (e4m3) GEMM grouped by expert, with ragged groups: rows offsets[e] ..
 // offsets[e + 1] - 1 of the output come from expert e's weights.  The arithmetic
 // is that of gemm_fp8.hip on the same instructions, so that a row has the bits that
-// the dense product with its expert's weights gives it.
+// the dense product with its expert's weights gives it: for a bf16 y those of the fp8
+// instruction, which cuts small products beside large ones, as explained there.
 //
 // The groups are known on the device only: the grid is the largest number of row
 // tiles that the sizes allow, each workgroup finds its tile from the offsets, and

@@ -469,7 +469,10 @@ int prism_route_experts(const void* logits, int type, int64_t ld, const float* b
  *           prism_quantize_tiles_fp8.
  *   y       [R][N] of y_type, output, aligned to its element size.  Rows in
  *           front of offsets[0] and from offsets[E] on are left as they are.
- * Row by row the bits of prism_gemm_fp8_blockscale with that expert's weights.
+ * Row by row the bits of prism_gemm_fp8_blockscale with that expert's weights: with
+ * y_type fp32 or fp16 from exact products, with bf16 from the matrix cores' fp8
+ * sums, whose error can reach 2^-6 of a block's largest product where products
+ * cancel, as said there.
  * Offsets are taken as clamped to 0 .. R; where they descend, what is written
  * of y is not specified (nothing else is).  E up to PRISM_EXPERTS_MAX, R up to
  * 2^31 - 257; with rows, M * K below 2^31.
