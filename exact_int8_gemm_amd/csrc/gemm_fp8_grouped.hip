@@ -209,10 +209,10 @@ int launch_wide(const Grouped& a, hipStream_t st, bool check) {
   return launch_status();
 }
 
-// Kernel for (R, E, N), fitted on MI355X with weights from HBM (us below, K = 2560; all
-// grow alike with K).  Groups are not known here: as many as can have rows are taken to,
-// each with half a tile more than its rows fill.  Estimates count rounds of the
-// tiles that run at once:
+// Kernel for (R, E, N), fitted on MI355X with weights from HBM (us below) at K = 2560 alone:
+// other K are taken to stretch all forms alike, which was not measured.  Groups are not
+// known here: as many as can have rows are taken to, each with half a tile more than
+// its rows fill.  Estimates count rounds of the tiles that run at once:
 //  * an fp32 or f16 y: the kernel for few rows while its workgroups are few (8
 //    groups of 6 rows by 2560 columns: 14.7, 64 x 64 tiles 18.3; of 16 rows 22.4 and
 //    18.9), else 64 x 64 or 128 x 128 tiles (64 groups by 640 columns: 48 rows 35 and

@@ -66,7 +66,8 @@ struct Norm {
 
 // A residual of this many bytes is written past the caches: it is read again behind a whole part of the
 // layer, whose weights alone are more than the caches hold (8192 x 5120, us: fp32
-// residual 80.5, through them 84.7; bf16, 84 MB, 54 both ways).
+// residual, 168 MB, 80.5, through them 84.7; bf16, 84 MB, 54 both ways; nothing in
+// between was measured).
 constexpr int64_t kPastBytes = (int64_t)128 << 20;
 
 // T: x's type and norm's; TR: the residual's, PAST: it is written past the caches.
