@@ -60,7 +60,7 @@ def parse(text):
 
 def is_copy(i):
     return i.name.startswith(("buffer_load", "global_load", "scratch_load")) and (
-        "_lds_" in i.name or i.operands[-1].split(" ")[-1] == "lds")
+        "_lds_" in i.name or "lds" in i.operands[-1].split(" "))
 
 
 def _vector_writes(i):

@@ -34,10 +34,12 @@ COPY = "buffer_load_dwordx4 v0, s[4:7], 0 offen lds"
     (["v_add_co_u32_e64 v1, s[6:7], v1, v2", "s_nop 0", COPY], 1),
     (["v_add_u32_e32 v1, s6, v1", "s_nop 0", COPY], 0),
     (["v_readlane_b32 s8, v9, 1", "buffer_load_dwordx4 v[0:3], v4, s[4:7], 0 offen"], 0),
+    (["s_mov_b32 m0, s1", "buffer_load_dword v0, s[4:7], 0 offen offset:64 lds sc0"], 1),
+    (["v_readlane_b32 s2, v9, 1", "s_nop 3", "global_load_lds_dwordx4 v0, s[2:3]"], 1),
     # over a branch: the write in front of the jump back, and one that no path leads on from
     (["s_nop 7", "s_nop 0", COPY, "s_nop 7", "v_readlane_b32 s4, v9, 1", "s_cbranch_scc0 9@<f+0x4>"], 1),
     (["s_branch 9@<f+0xc>", "v_readlane_b32 s4, v9, 1", "s_endpgm", COPY], 0)])
 def test_the_check_itself(lines, wrong):
     code = wait_states.parse(listing(*lines))["f"]
     copies, found = wait_states.too_early(code)
-    assert copies == sum(l.endswith("lds") for l in lines) and len(found) == wrong
+    assert copies == sum(" lds" in l for l in lines) and len(found) == wrong
