@@ -12,7 +12,7 @@
 // groups, 2560 x 4096 bf16, 110 us (625 MB and more: 5.7 TB/s); 1 x 8 of 64, 2560 x 2560,
 // 11.5 (52 MB, 4.6 TB/s).  Between them and the wide tiles, which are bound as the
 // dense product's are, short tiles whose rows are in part empty: 611 x 4 of 60, 2576 x
-// 1472 fp16, 69 us (48 for the bytes; VALU 59% active, MFMA 27% busy).
+// 1472 fp16, 69 us (48 for the bytes; VALU 58% active, MFMA 27% busy).
 #include "gemm_fp8_grouped_wide.h"
 
 namespace prism {

@@ -19,8 +19,8 @@
 // 32768 rows by 2560 x 2560 (430 GFLOP), us, tile_body's kernel and this one: one group
 // 220 and 197 (2.18 PFLOP/s), 16 ragged ones 249 and 225, 64 ragged ones 289 and 262.  A
 // stage of a tall tile takes 1.7 us, with 64 KB for each of 256 compute units, 9 to 10
-// TB/s out of the L2s, and 2.5 PFLOP/s, about what a large library product makes; that
-// of a lower tile takes not much less (192 rows 1.4, 128 rows 1.2: 2.3 and 1.8 PFLOP/s).
+// TB/s out of the L2s, and 2.5 PFLOP/s, what a large library product makes on a warm chip
+// (2.4 to 3.1); that of a lower tile takes not much less (192 rows 1.4, 128 rows 1.2: 2.3 and 1.8 PFLOP/s).
 // So ragged groups lose by their lower tiles, by the conversions and stores between
 // tiles, and by a list that is cut into equal numbers of tiles, not into equal work;
 // how much by each was not measured.  Weights from HBM add 0.4 us a stage.  Not kept: a list
